@@ -320,6 +320,87 @@ fmha_status fmha_quantize_nvfp4(const void* src, int64_t src_row_stride, int32_t
                                 int64_t codes_row_stride, uint8_t* block_scales, int64_t block_scales_row_stride,
                                 float* token_scales, int32_t fast_math, struct CUstream_st* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators over the K/V cache of a ragged batch (none of them is on the
+ * pages: additions of this library, written from their formulas below).
+ *
+ * The sequences of a batch differ in length, and the lengths live on the
+ * device, so a launch can be captured in a CUDA graph and replayed while the
+ * sequences grow. Nothing else of the conventions above changes: caller-owned
+ * memory, no state between calls, host checks before any launch, bounded
+ * device waits.                                                            */
+
+/* The cache and the queries of one call. Each operator names the members it
+ * reads; the others may be left zero.
+ *   k, v: contiguous [B, capacity, Hkv, D]; or, with a page_table, pools
+ *     [num_pages, page_size, Hkv, D] in which token s of sequence b is row
+ *     s % page_size of page page_table[b*max_pages_per_seq + s/page_size]
+ *     (int32, device; page_size 16, 32, 64 or 128). Dtypes (k, v): (BF16,
+ *     BF16), (BF16, E4M3) or (E4M3, E4M3), with sf_k / sf_v (E4M3 only) NONE,
+ *     PER_TENSOR or PER_HEAD [B, Hkv], positive and finite. D: 64 or 128.
+ *   q, o: BF16 [B, T, Hq, D]; query head h reads KV head h / (Hq / Hkv), for
+ *     any whole ratio.
+ *   capacity: tokens a sequence has room for; 0 with a page_table selects
+ *     max_pages_per_seq * page_size.
+ *   lens: int32 [B], device (see each operator).
+ *   q_lens: int32 [B], device, nullable (= T everywhere): query tokens in use,
+ *     the first q_lens[b] of the T. The rows of the others are padding: what q
+ *     holds there is not used, and they get O = 0 and lse = -inf.
+ *   softmax_scale <= 0 selects 1/sqrt(D).
+ *   lse (nullable): fp32 [B, Hq, T], natural-log log-sum-exp of the scaled
+ *     scores; -inf for a row that sees no key, whose O row is 0.
+ * What a row does not see never reaches it: keys past a sequence's end, or
+ * hidden nodes of a tree, may hold infinities or NaN.
+ * Device errors (fmha_get_device_error): FMHA_ERR_DEVICE_INDEX for a page or
+ * block index out of range (a bad page reads zeros, a bad block is left out),
+ * or a length outside the cache (cut to it).                               */
+typedef struct {
+  fmha_tensor q, k, v, o;
+  fmha_sf sf_k, sf_v;
+  int32_t B, T, Hq, Hkv, D, capacity;
+  const int32_t* lens;
+  const int32_t* q_lens;
+  const int32_t* page_table;
+  int32_t num_pages, page_size, max_pages_per_seq;
+  float softmax_scale;
+  float* lse;
+} fmha_cache_args;
+
+/* Attention of a tree of drafted tokens over the cache (speculative decoding:
+ * one pass scores every drafted continuation). Sequence b has lens[b] tokens
+ * of context, and its q_lens[b] nodes' keys and values stand right after them
+ * (node j at position lens[b] + j). Node i sees the whole context, and node j
+ * iff tree_mask says so:
+ *   tree_mask: uint8, byte (b, i, j) at tree_mask[b*mask_stride_b + i*T + j],
+ *     nonzero = node i sees node j (normally its ancestors and itself);
+ *     mask_stride_b may be 0 to share one tree. NULL = node i sees nodes 0..i:
+ *     a chain, which with T = 1 is one ordinary decoding step of a ragged
+ *     batch. A row may be empty.
+ *   lens[b] + q_lens[b] must not exceed the capacity.
+ *   workspace: device, 16-byte aligned, caller-owned, at least
+ *     fmha_fwd_tree_workspace_bytes(args) bytes; not shared with a call that
+ *     may overlap. A captured graph keeps using the one it was captured with.
+ * Rows of the result do not depend on the batch's other sequences but for the
+ * order in which parts of their sums are added.                            */
+fmha_status fmha_fwd_tree(const fmha_cache_args* args, const uint8_t* tree_mask, int64_t mask_stride_b,
+                          void* workspace, size_t workspace_bytes, struct CUstream_st* stream);
+size_t fmha_fwd_tree_workspace_bytes(const fmha_cache_args* args);
+
+/* Attention over the blocks of keys picked for each query token.
+ *   lens[b]: tokens in the cache, the q_lens[b] query tokens (its last ones)
+ *     among them: query token t stands at position lens[b] - q_lens[b] + t
+ *     and sees keys up to and including its own position.
+ *   blocks: int32 [B, T, Hkv, top] contiguous, device: ids of the blocks that
+ *     query token t reads in KV head h, in any order; block i is positions
+ *     [i*block, (i+1)*block), a negative id is no block. Ids are distinct (the
+ *     keys of a repeated id count each time). fmha_select_blocks makes them.
+ *   block: 16, 32, 64 or 128.
+ *   workspace: as for fmha_fwd_tree; may be NULL when
+ *     fmha_fwd_selected_workspace_bytes(args, top, block) is 0.             */
+fmha_status fmha_fwd_selected(const fmha_cache_args* args, const int32_t* blocks, int32_t top, int32_t block,
+                              void* workspace, size_t workspace_bytes, struct CUstream_st* stream);
+size_t fmha_fwd_selected_workspace_bytes(const fmha_cache_args* args, int32_t top, int32_t block);
+
 /* Workspace bytes fmha_fwd_decode needs for these args and num_splits
  * (0: a single split, or invalid sizes). Host only.                         */
 size_t fmha_decode_workspace_bytes(const fmha_args* args, int32_t num_splits);

@@ -22,6 +22,7 @@
 #include <mutex>
 
 #include "fmha_internal.h"
+#include "host_common.h"
 
 namespace fmha {
 cudaError_t launch_attention_bf16(int, bool, const AttnParams&, const CUtensorMap&, const CUtensorMap&,
@@ -56,6 +57,11 @@ __device__ uint32_t g_device_error_word;
 thread_local char g_msg[512] = "";
 std::atomic<uint64_t> g_wait_cycles{0};
 
+}  // namespace
+
+namespace fmha {
+namespace host {
+
 fmha_status fail(fmha_status s, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -67,6 +73,11 @@ fmha_status fail(fmha_status s, const char* fmt, ...) {
 fmha_status ok_status() {
   g_msg[0] = '\0';
   return FMHA_OK;
+}
+
+uint64_t wait_cycles() {
+  const uint64_t wc = g_wait_cycles.load();
+  return wc ? wc : kDefaultWaitCycles;
 }
 
 uint32_t* device_error_word(cudaError_t* err) {
@@ -91,10 +102,6 @@ uint32_t* device_error_word(cudaError_t* err) {
 }
 
 // ------------------------------------------------------ TMA descriptors ----
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 EncodeTiledFn encode_fn(cudaError_t* err) {
   static EncodeTiledFn fn = nullptr;
   static cudaError_t status = cudaSuccess;
@@ -110,43 +117,6 @@ EncodeTiledFn encode_fn(cudaError_t* err) {
   return fn;
 }
 
-// RANK-d map (dims innermost first, RANK = 4 or 5) with 128-byte swizzle.
-// Strides in elements for dims 1..RANK-1. Size-1 dims get a packed stride so
-// the descriptor stays valid whatever the caller's stride.
-template <int RANK>
-fmha_status make_map_n(CUtensorMap* map, void* base, int elem_bytes, const uint64_t (&dims)[RANK],
-                       const int64_t (&strides_elems)[RANK - 1], const uint32_t (&box)[RANK], const char* what,
-                       CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
-  cudaError_t e;
-  EncodeTiledFn fn = encode_fn(&e);
-  if (fn == nullptr) return fail(FMHA_ERR_CUDA, "cuTensorMapEncodeTiled unavailable: %s", cudaGetErrorString(e));
-  cuuint64_t gdim[RANK];
-  cuuint64_t gstride[RANK - 1];
-  cuuint32_t ebox[RANK];
-  cuuint32_t bdim[RANK];
-  uint64_t packed = dims[0] * elem_bytes;
-  for (int i = 0; i < RANK; ++i) {
-    gdim[i] = dims[i];
-    bdim[i] = box[i];
-    ebox[i] = 1;
-  }
-  for (int i = 0; i < RANK - 1; ++i) {
-    uint64_t s = static_cast<uint64_t>(strides_elems[i]) * elem_bytes;
-    if (dims[i + 1] == 1) s = (packed + 15) / 16 * 16;
-    gstride[i] = s;
-    packed = s * dims[i + 1];
-  }
-  const CUtensorMapDataType dt = elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  CUresult r = fn(map, dt, RANK, base, gdim, gstride, bdim, ebox, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(FMHA_ERR_INVALID_ARG, "TMA descriptor for %s rejected (CUresult %d)", what, (int)r);
-  return FMHA_OK;
-}
-fmha_status make_map(CUtensorMap* map, void* base, int elem_bytes, const uint64_t (&dims)[4],
-                     const int64_t (&strides_elems)[3], const uint32_t (&box)[4], const char* what) {
-  return make_map_n<4>(map, base, elem_bytes, dims, strides_elems, box, what);
-}
-
 int elem_bytes(int dt) {
   switch (dt) {
     case FMHA_BF16:
@@ -158,9 +128,6 @@ int elem_bytes(int dt) {
   }
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Checks a [B, S, H, D] operand: pointer, alignment, strides. Size-1 dims' strides are free.
 fmha_status check_tensor(const fmha_tensor& t, const char* name, int B, int S, int H, int D) {
   if (t.reserved != 0) return fail(FMHA_ERR_INVALID_ARG, "%s.reserved must be 0", name);
   const int eb = elem_bytes(t.dtype);
@@ -180,8 +147,6 @@ fmha_status check_tensor(const fmha_tensor& t, const char* name, int B, int S, i
     return fail(FMHA_ERR_INVALID_ARG, "%s.stride_h smaller than D (rows overlap)", name);
   return FMHA_OK;
 }
-
-int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 fmha_status check_sf(const fmha_sf& sf, const char* name, bool allow_head, bool allow_tensor, bool allow_block,
                      int block_multiple, bool allow_channel) {
@@ -209,6 +174,25 @@ fmha_status check_sf(const fmha_sf& sf, const char* name, bool allow_head, bool 
   return FMHA_OK;
 }
 
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+  return n;
+}
+
+}  // namespace host
+}  // namespace fmha
+
+namespace {
+
+using namespace fmha::host;
+
+fmha_status make_map(CUtensorMap* map, void* base, int elem_bytes, const uint64_t (&dims)[4],
+                     const int64_t (&strides_elems)[3], const uint32_t (&box)[4], const char* what) {
+  return make_map_n<4>(map, base, elem_bytes, dims, strides_elems, box, what);
+}
+
 struct PagedArgs {
   const int32_t* page_table;
   int32_t num_pages, page_size, max_pages_per_seq;
@@ -219,13 +203,6 @@ struct DecodeArgs {
   void* workspace;
   size_t workspace_bytes;
 };
-
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
-  return n;
-}
 
 // The decode path packs Sq * (Hq / Hkv) query rows per KV head, counted in 32 bits.
 bool packed_rows_fit(int Sq, int Hq, int Hkv) {
@@ -423,8 +400,7 @@ fmha_status run_attention(const fmha_args* a, const uint8_t* mask, int64_t msb, 
   cudaError_t e;
   p.err = device_error_word(&e);
   if (p.err == nullptr) return fail(FMHA_ERR_CUDA, "device error word: %s", cudaGetErrorString(e));
-  const uint64_t wc = g_wait_cycles.load();
-  p.wait_cycles = wc ? wc : kDefaultWaitCycles;
+  p.wait_cycles = wait_cycles();
 
   if (packed) {
     const SplitPlan sp = plan_splits(B, Hq, Hkv, Sq, Skv, D, dec->num_splits);
@@ -608,8 +584,7 @@ fmha_status quantize_impl(const fmha_tensor* src, const float* shift, const fmha
   cudaError_t e;
   p.err = device_error_word(&e);
   if (p.err == nullptr) return fail(FMHA_ERR_CUDA, "device error word: %s", cudaGetErrorString(e));
-  const uint64_t wc = g_wait_cycles.load();
-  p.wait_cycles = wc ? wc : kDefaultWaitCycles;
+  p.wait_cycles = wait_cycles();
   // Token blocks of at most 32 KB whose rows TMA can address (16-byte strides,
   // D <= 256 elements per box row, D / 8 a power of two) are staged whole in
   // shared memory by TMA.
@@ -738,6 +713,7 @@ fmha_status fmha_get_device_error(cudaStream_t stream) {
     return fail(FMHA_ERR_CUDA, "clear error word: %s", cudaGetErrorString(e));
   if (word & kErrTimeout) return fail(FMHA_ERR_TIMEOUT, "a kernel wait ran out (error word 0x%x)", word);
   if (word & kErrPageIndex) return fail(FMHA_ERR_DEVICE_INDEX, "a page-table entry was out of range");
+  if (word & kErrLength) return fail(FMHA_ERR_DEVICE_INDEX, "a sequence length was outside the cache");
   return ok_status();
 }
 

@@ -1,0 +1,272 @@
+// api_cache.cu -- C ABI of the operators over a ragged K/V cache: argument
+// checks, TMA descriptors and launch shapes (include/fmha.h).
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "cache_internal.h"
+#include "host_common.h"
+
+namespace {
+
+using namespace fmha;
+using namespace fmha::host;
+
+constexpr int kTile = 64;  // keys of one tile of the few-row kernels
+
+int log2_of(int v) {
+  int s = 0;
+  while ((1 << s) < v) ++s;
+  return s;
+}
+
+// Checks what every operator over the cache reads (need_v: V too; need_q: the
+// queries), and fills the view. *k8 / *v8: E4M3 keys / values.
+fmha_status check_cache(const fmha_cache_args* a, bool need_q, bool need_v, CacheView* c, bool* k8, bool* v8) {
+  const int B = a->B, T = a->T, Hq = a->Hq, Hkv = a->Hkv, D = a->D;
+  memset(c, 0, sizeof(*c));
+  if (D != 64 && D != 128) return fail(FMHA_ERR_UNSUPPORTED, "head dim %d (supported: 64, 128)", D);
+  if (need_q && (Hkv == 0 || Hq % Hkv != 0))
+    return fail(FMHA_ERR_INVALID_ARG, "Hq (%d) must be a multiple of Hkv (%d)", Hq, Hkv);
+  *k8 = a->k.dtype == FMHA_E4M3;
+  if (!*k8 && a->k.dtype != FMHA_BF16) return fail(FMHA_ERR_UNSUPPORTED, "K dtype %d unsupported", a->k.dtype);
+  fmha_status st;
+  if ((st = check_sf(a->sf_k, "sf_k", *k8, *k8, false, 1, false)) != FMHA_OK) return st;
+  if (need_v) {
+    *v8 = a->v.dtype == FMHA_E4M3;
+    if (!*v8 && a->v.dtype != FMHA_BF16) return fail(FMHA_ERR_UNSUPPORTED, "V dtype %d unsupported", a->v.dtype);
+    if (*k8 && !*v8) return fail(FMHA_ERR_UNSUPPORTED, "E4M3 keys need E4M3 values");
+    if ((st = check_sf(a->sf_v, "sf_v", *v8, *v8, false, 1, false)) != FMHA_OK) return st;
+  }
+  int capacity = a->capacity;
+  if (capacity < 0) return fail(FMHA_ERR_INVALID_ARG, "negative capacity");
+  if (a->page_table != nullptr) {
+    if (a->page_size != 16 && a->page_size != 32 && a->page_size != 64 && a->page_size != 128)
+      return fail(FMHA_ERR_UNSUPPORTED, "page_size %d (supported: 16, 32, 64, 128)", a->page_size);
+    if (a->num_pages <= 0) return fail(FMHA_ERR_INVALID_ARG, "num_pages must be positive");
+    if (a->max_pages_per_seq < 0) return fail(FMHA_ERR_INVALID_ARG, "negative max_pages_per_seq");
+    if (reinterpret_cast<uintptr_t>(a->page_table) & 3u) return fail(FMHA_ERR_INVALID_ARG, "page_table misaligned");
+    const int64_t room = static_cast<int64_t>(a->max_pages_per_seq) * a->page_size;
+    if (room > INT32_MAX / 2) return fail(FMHA_ERR_UNSUPPORTED, "more than 2^30 tokens per sequence");
+    if (capacity == 0) capacity = static_cast<int>(room);
+    if (capacity > room) return fail(FMHA_ERR_INVALID_ARG, "capacity %d exceeds the page table's %d", capacity, (int)room);
+  }
+  if (capacity > INT32_MAX / 2) return fail(FMHA_ERR_UNSUPPORTED, "more than 2^30 tokens per sequence");
+  if (a->lens == nullptr || (reinterpret_cast<uintptr_t>(a->lens) & 3u))
+    return fail(FMHA_ERR_INVALID_ARG, "lens is NULL or misaligned");
+  if (reinterpret_cast<uintptr_t>(a->q_lens) & 3u) return fail(FMHA_ERR_INVALID_ARG, "q_lens misaligned");
+  if (reinterpret_cast<uintptr_t>(a->lse) & 3u) return fail(FMHA_ERR_INVALID_ARG, "lse misaligned");
+  if (capacity > 0) {
+    const int n = a->page_table != nullptr ? a->num_pages : B;
+    const int s = a->page_table != nullptr ? a->page_size : capacity;
+    if ((st = check_tensor(a->k, "k", n, s, Hkv, D)) != FMHA_OK) return st;
+    if (need_v && (st = check_tensor(a->v, "v", n, s, Hkv, D)) != FMHA_OK) return st;
+  }
+  if (need_q) {
+    if (a->q.dtype != FMHA_BF16) return fail(FMHA_ERR_UNSUPPORTED, "q must be BF16");
+    if ((st = check_tensor(a->q, "q", B, T, Hq, D)) != FMHA_OK) return st;
+    if (static_cast<int64_t>(T) * (Hq / Hkv) > INT32_MAX / 2)
+      return fail(FMHA_ERR_UNSUPPORTED, "T * Hq / Hkv rows exceed 2^30");
+  }
+  c->B = B; c->T = T; c->Hq = Hq; c->Hkv = Hkv; c->G = need_q ? Hq / Hkv : 1;
+  c->capacity = capacity;
+  c->lens = a->lens;
+  c->q_lens = a->q_lens;
+  c->page_table = capacity > 0 ? a->page_table : nullptr;
+  c->num_pages = a->num_pages;
+  c->page_shift = a->page_table != nullptr ? log2_of(a->page_size) : 0;
+  c->max_pages = a->max_pages_per_seq;
+  cudaError_t e;
+  c->err = device_error_word(&e);
+  if (c->err == nullptr) return fail(FMHA_ERR_CUDA, "device error word: %s", cudaGetErrorString(e));
+  c->wait_cycles = wait_cycles();
+  return FMHA_OK;
+}
+
+// TMA map of K or V: boxes of `rows` tokens of one KV head and one swizzle column.
+fmha_status cache_map(CUtensorMap* m, const fmha_cache_args* a, const CacheView& c, const fmha_tensor& t, bool e8,
+                      int rows, const char* what) {
+  const int eb = e8 ? 1 : 2;
+  const int span = std::min(128, a->D * eb);
+  const bool paged = c.page_table != nullptr;
+  const uint64_t dims[4] = {uint64_t(a->D), uint64_t(a->Hkv), uint64_t(paged ? a->page_size : c.capacity),
+                            uint64_t(paged ? a->num_pages : a->B)};
+  const int64_t strides[3] = {t.stride_h, t.stride_s, t.stride_b};
+  const uint32_t box[4] = {uint32_t(span / eb), 1, uint32_t(rows), 1};
+  return make_map_n<4>(m, t.ptr, eb, dims, strides, box, what,
+                       span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+// The sizes of an attention call that do not need the device: grid and row
+// tiles of the tree form.
+struct TreePlan {
+  int rows, row_tiles, n_ctas;
+  size_t workspace_bytes;
+};
+constexpr int kMinTiles = 2;  // least key tiles of a CTA
+bool tree_plan(const fmha_cache_args* a, int capacity, TreePlan* t) {
+  const int64_t packed = static_cast<int64_t>(a->T) * (a->Hq / a->Hkv);
+  t->rows = cache_attn_rows(static_cast<int>(std::min<int64_t>(packed, 1 << 20)));
+  t->row_tiles = static_cast<int>((packed + t->rows - 1) / t->rows);
+  const int64_t items = static_cast<int64_t>(a->B) * a->Hkv * t->row_tiles;
+  const int64_t tiles = items * ceil_div(std::max(capacity, 1), kTile);
+  // Two CTAs fit an SM; more than one CTA per kMinTiles tiles has nothing to do.
+  t->n_ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(2 * sm_count(), (tiles + kMinTiles - 1) / kMinTiles)));
+  t->workspace_bytes = size_t(2) * t->n_ctas * t->rows * (size_t(a->D) + 1) * 4;
+  return items < (int64_t(1) << 31) && tiles / t->n_ctas < (int64_t(1) << 30);
+}
+
+struct PickPlan {
+  int rows, row_tiles, item_tiles, n_splits, per_split, n_ctas;
+  size_t workspace_bytes;
+};
+bool pick_plan(const fmha_cache_args* a, int top, int block, PickPlan* t) {
+  const int G = a->Hq / a->Hkv;
+  t->rows = cache_attn_rows(G);
+  t->row_tiles = ceil_div(G, t->rows);
+  const int64_t items = static_cast<int64_t>(a->B) * a->T * a->Hkv * t->row_tiles;
+  t->item_tiles = static_cast<int>((static_cast<int64_t>(top) * block + kTile - 1) / kTile);
+  const int target = 2 * sm_count();
+  int splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(target / std::max<int64_t>(1, items), t->item_tiles)));
+  t->per_split = ceil_div(t->item_tiles, splits);
+  t->n_splits = ceil_div(t->item_tiles, t->per_split);
+  t->n_ctas = static_cast<int>(std::min<int64_t>(items * t->n_splits, t->n_splits > 1 ? items * t->n_splits : target));
+  t->workspace_bytes = t->n_splits > 1 ? size_t(2) * t->n_ctas * t->rows * (size_t(a->D) + 1) * 4 : 0;
+  return items < (int64_t(1) << 31);
+}
+
+bool sizes_ok(const fmha_cache_args* a) {
+  return a != nullptr && a->B >= 0 && a->T >= 0 && a->Hq >= 0 && a->Hkv >= 0 && a->D >= 0;
+}
+// Queries that divide over the KV heads, and rows that fit 32 bits.
+bool rows_ok(const fmha_cache_args* a) {
+  return sizes_ok(a) && a->B > 0 && a->T > 0 && a->Hq > 0 && a->Hkv > 0 && a->Hq % a->Hkv == 0 &&
+         static_cast<int64_t>(a->T) * (a->Hq / a->Hkv) <= INT32_MAX / 2;
+}
+int64_t capacity_of(const fmha_cache_args* a) {
+  if (a->capacity != 0 || a->page_table == nullptr) return a->capacity;
+  return static_cast<int64_t>(a->max_pages_per_seq) * a->page_size;
+}
+
+fmha_status check_workspace(const void* ws, size_t have, size_t need) {
+  if (need == 0) return FMHA_OK;
+  if (ws == nullptr || !aligned16(ws)) return fail(FMHA_ERR_INVALID_ARG, "workspace is NULL or not 16-byte aligned");
+  if (have < need) return fail(FMHA_ERR_INVALID_ARG, "workspace of %zu bytes < %zu needed", have, need);
+  return FMHA_OK;
+}
+
+// Fills what the tree and the picked form share, with the TMA maps.
+fmha_status fill_attn(const fmha_cache_args* a, CacheAttnParams* p, bool* k8, bool* v8, int piece, CUtensorMap* tk,
+                      CUtensorMap* tv) {
+  fmha_status st;
+  memset(p, 0, sizeof(*p));
+  if ((st = check_cache(a, true, true, &p->c, k8, v8)) != FMHA_OK) return st;
+  if (a->o.dtype != FMHA_BF16) return fail(FMHA_ERR_UNSUPPORTED, "o must be BF16");
+  if ((st = check_tensor(a->o, "o", a->B, a->T, a->Hq, a->D)) != FMHA_OK) return st;
+  p->q = static_cast<const uint16_t*>(a->q.ptr);
+  p->q_sb = a->q.stride_b; p->q_ss = a->q.stride_s; p->q_sh = a->q.stride_h;
+  p->o = static_cast<uint16_t*>(a->o.ptr);
+  p->o_sb = a->o.stride_b; p->o_ss = a->o.stride_s; p->o_sh = a->o.stride_h;
+  p->lse = a->lse;
+  const float scale = a->softmax_scale > 0.f ? a->softmax_scale : 1.0f / std::sqrt(float(a->D));
+  p->scale_log2 = scale * 1.4426950408889634f;
+  p->sf_k = a->sf_k.ptr; p->sf_k_kind = a->sf_k.kind;
+  p->sf_v = a->sf_v.ptr; p->sf_v_kind = a->sf_v.kind;
+  piece = std::min(piece, kTile);
+  if (p->c.page_table != nullptr) piece = std::min(piece, a->page_size);
+  p->piece_shift = log2_of(piece);
+  if (p->c.capacity == 0) {  // no key is ever loaded; any valid map will do
+    const uint64_t dims[4] = {uint64_t(a->D), 1, 1, 1};
+    const int64_t strides[3] = {a->D, a->D, a->D};
+    const uint32_t box[4] = {64, 1, 1, 1};
+    if ((st = make_map_n<4>(tk, a->q.ptr, 2, dims, strides, box, "q")) != FMHA_OK) return st;
+    *tv = *tk;
+    return FMHA_OK;
+  }
+  if ((st = cache_map(tk, a, p->c, a->k, *k8, piece, "k")) != FMHA_OK) return st;
+  return cache_map(tv, a, p->c, a->v, *v8, piece, "v");
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fmha_fwd_tree_workspace_bytes(const fmha_cache_args* a) {
+  if (!rows_ok(a) || capacity_of(a) < 0 || capacity_of(a) > INT32_MAX / 2) return 0;
+  TreePlan t;
+  return tree_plan(a, static_cast<int>(capacity_of(a)), &t) ? t.workspace_bytes : 0;
+}
+
+fmha_status fmha_fwd_tree(const fmha_cache_args* a, const uint8_t* tree_mask, int64_t mask_stride_b, void* workspace,
+                          size_t workspace_bytes, cudaStream_t stream) {
+  if (a == nullptr) return fail(FMHA_ERR_INVALID_ARG, "args is NULL");
+  if (!sizes_ok(a)) return fail(FMHA_ERR_INVALID_ARG, "negative size");
+  if (a->B == 0 || a->T == 0 || a->Hq == 0) return ok_status();  // nothing to compute
+  if (mask_stride_b < 0) return fail(FMHA_ERR_INVALID_ARG, "mask stride must be >= 0");
+  CacheAttnParams p;
+  CUtensorMap tk, tv;
+  bool k8, v8;
+  fmha_status st;
+  if ((st = fill_attn(a, &p, &k8, &v8, kTile, &tk, &tv)) != FMHA_OK) return st;
+  TreePlan t;
+  if (!tree_plan(a, p.c.capacity, &t)) return fail(FMHA_ERR_UNSUPPORTED, "grid too large");
+  if ((st = check_workspace(workspace, workspace_bytes, t.workspace_bytes)) != FMHA_OK) return st;
+  p.mask = tree_mask;
+  p.mask_sb = mask_stride_b;
+  p.row_tiles = t.row_tiles;
+  p.n_ctas = t.n_ctas;
+  p.min_tiles = kMinTiles;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_lse = p.part_o + size_t(2) * t.n_ctas * t.rows * a->D;
+  cudaError_t e = launch_cache_attn(a->D, k8, v8, p, tk, tv, stream);
+  if (e == cudaSuccess) e = launch_cache_merge(a->D, p, stream);
+  if (e != cudaSuccess) return fail(FMHA_ERR_CUDA, "tree attention launch: %s", cudaGetErrorString(e));
+  return ok_status();
+}
+
+size_t fmha_fwd_selected_workspace_bytes(const fmha_cache_args* a, int32_t top, int32_t block) {
+  if (!rows_ok(a) || top <= 0 || block <= 0 || static_cast<int64_t>(top) * block > INT32_MAX / 2) return 0;
+  PickPlan t;
+  return pick_plan(a, top, block, &t) ? t.workspace_bytes : 0;
+}
+
+fmha_status fmha_fwd_selected(const fmha_cache_args* a, const int32_t* blocks, int32_t top, int32_t block,
+                              void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (a == nullptr) return fail(FMHA_ERR_INVALID_ARG, "args is NULL");
+  if (!sizes_ok(a)) return fail(FMHA_ERR_INVALID_ARG, "negative size");
+  if (a->B == 0 || a->T == 0 || a->Hq == 0) return ok_status();  // nothing to compute
+  if (block != 16 && block != 32 && block != 64 && block != 128)
+    return fail(FMHA_ERR_UNSUPPORTED, "block %d (supported: 16, 32, 64, 128)", block);
+  if (top <= 0 || static_cast<int64_t>(top) * block > INT32_MAX / 2)
+    return fail(FMHA_ERR_INVALID_ARG, "top %d out of range", top);
+  if (blocks == nullptr || (reinterpret_cast<uintptr_t>(blocks) & 3u))
+    return fail(FMHA_ERR_INVALID_ARG, "blocks is NULL or misaligned");
+  CacheAttnParams p;
+  CUtensorMap tk, tv;
+  bool k8, v8;
+  fmha_status st;
+  if ((st = fill_attn(a, &p, &k8, &v8, block, &tk, &tv)) != FMHA_OK) return st;
+  PickPlan t;
+  if (!pick_plan(a, top, block, &t)) return fail(FMHA_ERR_UNSUPPORTED, "grid too large");
+  if ((st = check_workspace(workspace, workspace_bytes, t.workspace_bytes)) != FMHA_OK) return st;
+  p.blocks = blocks;
+  p.top = top;
+  p.block_shift = log2_of(block);
+  p.n_blocks = ceil_div(p.c.capacity, block);
+  p.row_tiles = t.row_tiles;
+  p.n_ctas = t.n_ctas;
+  p.item_tiles = t.item_tiles;
+  p.n_splits = t.n_splits;
+  p.per_split = t.per_split;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_lse = p.part_o + size_t(2) * t.n_ctas * t.rows * a->D;
+  cudaError_t e = launch_cache_attn(a->D, k8, v8, p, tk, tv, stream);
+  if (e == cudaSuccess && t.n_splits > 1) e = launch_cache_merge(a->D, p, stream);
+  if (e != cudaSuccess) return fail(FMHA_ERR_CUDA, "picked-block attention launch: %s", cudaGetErrorString(e));
+  return ok_status();
+}
+
+}  // extern "C"

@@ -1,0 +1,834 @@
+// cache_attn.cu -- attention of a few query rows per KV head over a ragged,
+// paged (or contiguous) K/V cache: a tree of drafted tokens after each
+// sequence's context (one node: ordinary decoding), or the blocks of keys
+// picked for each query token.
+//
+// O_r = sum_s p_rs V_s / l_r, p_rs = exp2(c q_r . k_s - m_r), l_r = sum_s p_rs,
+// over the keys row r sees, in one pass over the keys with the running row
+// maximum m. Rows are (query token, head of the KV head's group), so a K/V
+// tile is read once for all query heads that share it.
+//
+// Work: items (sequence, [token,] KV head, row tile) x 64-key tiles. In tree
+// mode the tiles of all items form one list that the CTAs share evenly, so a
+// batch of very different lengths keeps every SM busy; the lengths are read on
+// the device, and a launch can be captured and replayed with others. A CTA
+// holds at most two partial items (its first and its last); their O / l and
+// log-sum-exp go to the workspace and a second kernel merges them.
+//
+// 160 threads: four MMA warps and one TMA producer warp feeding a ring of
+// 64-key slots. A warp takes 16 rows; with at most 16 rows the four warps take
+// 16 keys of the slot each (own m, l, O, joined at the item's end), with 32
+// rows two and two, with 64 rows every warp takes all keys.
+#include <cuda_fp16.h>
+
+#include "cache_tiles.cuh"
+#include "mma_sync.cuh"
+
+namespace fmha {
+namespace {
+
+constexpr uint32_t kFull = 0xffffffffu;
+
+template <int D_, bool K8_, bool V8_, int WM_, bool PICKED_>
+struct CaCfg {
+  static constexpr int D = D_, WM = WM_, WN = 4 / WM_;
+  static constexpr bool K8 = K8_, V8 = V8_, PICKED = PICKED_;
+  using KL = TileLayout<D, K8>;
+  using VL = TileLayout<D, V8>;
+  static constexpr int ROWS = 16 * WM;
+  static constexpr int SLOT = KL::BYTES + VL::BYTES;
+  static constexpr int STAGES = SLOT >= 32768 ? 3 : SLOT >= 24576 ? 4 : SLOT >= 16384 ? 6 : 8;
+  static constexpr int RED_LD = 36;  // floats per row of the joining buffer (32 columns + padding)
+  static constexpr int RED_BYTES = 4 * 16 * RED_LD * 4;
+  static constexpr int SMEM = STAGES * SLOT + RED_BYTES + 2048;
+  static constexpr int THREADS = 160;
+};
+
+template <int STAGES>
+struct alignas(16) CaMisc {
+  uint64_t full[STAGES], empty[STAGES];
+  TileMeta meta[STAGES];
+  float ml[4][16][2];  // (m, l) of each warp's rows
+  volatile uint32_t abort;
+};
+
+// A run of key tiles [t0, t1) of one item.
+struct Seg {
+  int b, t, hkv, rt;
+  int t0, t1, nt;
+  int ctx, nodes;  // tree: context length and nodes in use
+  int limit;       // picked: keys at or past it are hidden
+};
+
+// The list of key tiles, shared evenly: CTA i takes tiles [i per, (i + 1) per).
+struct Share {
+  long long total;
+  int per;
+};
+
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+__device__ __forceinline__ int tiles_of(const SeqLens s) { return (s.len + s.q + kTileKeys - 1) / kTileKeys; }
+
+// Whole warp. Tiles of sequences [0, n), per (KV head, row tile).
+__device__ long long tree_tiles(const CacheAttnParams& p, int n, bool report) {
+  long long sum = 0;
+  for (int b = threadIdx.x & 31; b < n; b += 32) {
+    bool bad;
+    sum += tiles_of(tree_lens(p.c, b, bad));
+    if (bad && report) atomicOr(p.c.err, kErrLength);
+  }
+  return warp_sum(sum);
+}
+__device__ Share tree_share(const CacheAttnParams& p, bool report) {
+  Share s;
+  s.total = tree_tiles(p, p.c.B, report) * p.c.Hkv * p.row_tiles;
+  s.per = static_cast<int>((s.total + p.n_ctas - 1) / p.n_ctas);
+  s.per = max(s.per, p.min_tiles);
+  return s;
+}
+
+// Walks a CTA's segments; every warp keeps its own copy.
+template <bool PICKED>
+struct Walk {
+  long long pos, end;    // tree: tiles of the list; picked: items
+  int b;                 // tree: current sequence, its first tile in the list and its tiles per item
+  long long base;
+  int nt;
+  SeqLens len;
+
+  __device__ void start(const CacheAttnParams& p) {
+    if constexpr (PICKED) {
+      pos = blockIdx.x;
+      end = static_cast<long long>(p.c.B) * p.c.T * p.c.Hkv * p.row_tiles * p.n_splits;
+    } else {
+      const Share s = tree_share(p, blockIdx.x == 0);
+      pos = min(s.total, static_cast<long long>(blockIdx.x) * s.per);
+      end = min(s.total, pos + s.per);
+      b = -1;
+      base = 0;
+      nt = 0;
+    }
+  }
+
+  __device__ bool next(const CacheAttnParams& p, Seg& g) {
+    if (pos >= end) return false;
+    if constexpr (PICKED) {
+      long long item = pos / p.n_splits;
+      const int j = static_cast<int>(pos - item * p.n_splits);
+      pos += gridDim.x;
+      g.rt = static_cast<int>(item % p.row_tiles);
+      item /= p.row_tiles;
+      g.hkv = static_cast<int>(item % p.c.Hkv);
+      item /= p.c.Hkv;
+      g.t = static_cast<int>(item % p.c.T);
+      g.b = static_cast<int>(item / p.c.T);
+      g.nt = p.item_tiles;
+      g.t0 = min(g.nt, j * p.per_split);
+      g.t1 = min(g.nt, g.t0 + p.per_split);
+      bool bad;
+      const SeqLens s = seq_lens(p.c, g.b, bad);
+      if (bad && g.t == 0 && g.hkv == 0) atomicOr(p.c.err, kErrLength);
+      g.limit = g.t < s.q ? s.len - s.q + g.t + 1 : 0;
+      g.ctx = 0x7fffffff;
+      g.nodes = 0;
+    } else {
+      const int lane = threadIdx.x & 31;
+      const int items = p.c.Hkv * p.row_tiles;  // per sequence
+      while (b < 0 || pos >= base + static_cast<long long>(nt) * items) {
+        // 32 sequences at a time: the first whose tiles reach past pos
+        if (b >= 0) base += static_cast<long long>(nt) * items;
+        const int first = b + 1;
+        bool bad;
+        const int bb = first + lane;
+        const SeqLens s = bb < p.c.B ? tree_lens(p.c, bb, bad) : SeqLens{0, 0};
+        const int n = tiles_of(s);
+        int run = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(kFull, run, o);
+          if (lane >= o) run += v;
+        }
+        const uint32_t past = __ballot_sync(kFull, base + static_cast<long long>(run) * items > pos);
+        const int k = past ? __ffs(past) - 1 : 31;
+        base += static_cast<long long>(__shfl_sync(kFull, run - n, k)) * items;
+        nt = __shfl_sync(kFull, n, k);
+        len.len = __shfl_sync(kFull, s.len, k);
+        len.q = __shfl_sync(kFull, s.q, k);
+        b = first + k;
+        if (b >= p.c.B) return false;  // not reached: pos < total
+      }
+      const long long x = pos - base;
+      const int item = static_cast<int>(x / nt);
+      g.b = b;
+      g.t = 0;
+      g.rt = item % p.row_tiles;
+      g.hkv = item / p.row_tiles;
+      g.nt = nt;
+      g.t0 = static_cast<int>(x - static_cast<long long>(item) * nt);
+      g.t1 = static_cast<int>(min(static_cast<long long>(nt), g.t0 + (end - pos)));
+      g.ctx = len.len;
+      g.nodes = len.q;
+      g.limit = len.len + len.q;
+      pos += g.t1 - g.t0;
+    }
+    return true;
+  }
+};
+
+// ---------------------------------------------------------------- producer --
+template <class C>
+__device__ void produce(const CacheAttnParams& p, uint8_t* ring, CaMisc<C::STAGES>* misc, const CUtensorMap* tk,
+                        const CUtensorMap* tv, const Waiter w) {
+  using namespace ptx;
+  const int lane = threadIdx.x & 31;
+  const int ps = p.piece_shift, ppt = kTileKeys >> ps;  // pieces per tile
+  constexpr int COPIES = C::KL::CHUNKS + C::VL::CHUNKS;
+  const int my_piece = lane / COPIES, my_copy = lane - my_piece * COPIES;
+  uint32_t it = 0;
+  bool ok = true;
+  Walk<C::PICKED> walk;
+  walk.start(p);
+  Seg g;
+  while (ok && walk.next(p, g)) {
+    // Lane l holds piece `first + l` of the item; the next 32 are fetched early.
+    auto fetch = [&](int i) {
+      Piece e{0, 0, 0, 0};
+      if (i >= g.t1 * ppt) return e;
+      if constexpr (C::PICKED) {
+        const int k = p.block_shift - ps;  // pieces per block, log2
+        const int slot = i >> k;
+        if (slot >= p.top) return e;
+        const int id = __ldg(p.blocks + ((static_cast<int64_t>(g.b) * p.c.T + g.t) * p.c.Hkv + g.hkv) * p.top + slot);
+        if (id >= p.n_blocks) atomicOr(p.c.err, kErrPageIndex);
+        if (id < 0 || id >= p.n_blocks) return e;
+        return cache_piece(p.c, g.b, (id << p.block_shift) + ((i & ((1 << k) - 1)) << ps), g.limit);
+      } else {
+        return cache_piece(p.c, g.b, i << ps, g.limit);
+      }
+    };
+    int first = g.t0 * ppt;
+    Piece cur = fetch(first + lane), nxt = fetch(first + 32 + lane);
+    for (int u = g.t0; u < g.t1; ++u) {
+      if (u * ppt - first >= 32) {
+        first += 32;
+        cur = nxt;
+        nxt = fetch(first + 32 + lane);
+      }
+      const int at = u * ppt - first;  // lane of this tile's first piece
+      const int s = it % C::STAGES;
+      const uint32_t ph = (it / C::STAGES) & 1;
+      if (!(ok = __all_sync(kFull, w.wait(smem_addr(&misc->empty[s]), ph ^ 1)))) break;
+      ++it;
+      {  // lanes 0..3: the tile's 16-key groups
+        const int sub = (lane & 3) << 4;
+        const int src = at + (sub >> ps);
+        const int pos = __shfl_sync(kFull, cur.pos, src) + (sub & ((1 << ps) - 1));
+        const int valid = __shfl_sync(kFull, cur.valid, src) - (sub & ((1 << ps) - 1));
+        if (lane < kGroups) {
+          misc->meta[s].pos[lane] = pos;
+          misc->meta[s].valid[lane] = min(16, max(0, valid));
+        }
+      }
+      const int src = (at + my_piece) & 31;
+      const int row = __shfl_sync(kFull, cur.row, src), outer = __shfl_sync(kFull, cur.outer, src);
+      const bool live = __shfl_sync(kFull, cur.valid, src) > 0 && my_piece < ppt;
+      const uint32_t n = __popc(__ballot_sync(kFull, live && my_copy == 0));
+      const uint32_t full = smem_addr(&misc->full[s]);
+      if (lane == 0) mbar_arrive_expect_tx(full, (n << ps) * (C::KL::ROW + C::VL::ROW));
+      __syncwarp();
+      if (live) {
+        const uint32_t base = smem_addr(ring + s * C::SLOT);
+        if (my_copy < C::KL::CHUNKS)
+          tma_load_4d(base + my_copy * C::KL::CHUNK_BYTES + (my_piece << ps) * C::KL::SPAN, tk, full,
+                      my_copy * C::KL::CHUNK_ELEMS, g.hkv, row, outer);
+        else
+          tma_load_4d(base + C::KL::BYTES + (my_copy - C::KL::CHUNKS) * C::VL::CHUNK_BYTES +
+                          (my_piece << ps) * C::VL::SPAN,
+                      tv, full, (my_copy - C::KL::CHUNKS) * C::VL::CHUNK_ELEMS, g.hkv, row, outer);
+      }
+    }
+  }
+  // Every copy has landed before shared memory goes away.
+  if (lane == 0)
+    for (uint32_t k = it > C::STAGES ? it - C::STAGES : 0; k < it; ++k)
+      w.drain(smem_addr(&misc->full[k % C::STAGES]), (k / C::STAGES) & 1u);
+  __syncwarp();
+}
+
+// --------------------------------------------------------------- MMA warps --
+// A row's query token and head; token < 0: padding.
+struct Row {
+  int tok, head;
+};
+template <class C>
+__device__ __forceinline__ Row row_of(const CacheAttnParams& p, const Seg& g, int r) {
+  const int i = g.rt * C::ROWS + r;
+  if constexpr (C::PICKED) return i < p.c.G ? Row{g.t, g.hkv * p.c.G + i} : Row{-1, 0};
+  const int t = i / p.c.G;
+  return t < p.c.T ? Row{t, g.hkv * p.c.G + i - t * p.c.G} : Row{-1, 0};
+}
+
+// Two fp32 -> the 16-bit pair the PV product takes.
+template <class C>
+__device__ __forceinline__ uint32_t pack_p(float a, float b) {
+  return C::V8 ? ptx::pack_f16x2(a, b) : ptx::pack_bf16x2(a, b);
+}
+
+// V fragments (keys 16 x columns 32q .. 32q + 31) as four n-tiles: b0 holds
+// keys 2j, 2j + 1 and b1 keys 2j + 8, 2j + 9 of a column. BF16: n-tile i is
+// columns 32q + 8i ..; E4M3: lane group g's column of n-tile i is 32q + 4g + i
+// (four neighbouring codes of a key come in one word), converted to F16, which
+// holds every E4M3 value.
+template <class C>
+__device__ __forceinline__ void load_v(uint32_t (&b)[4][2], uint32_t v_base, int key0, int q, int lane) {
+  using namespace ptx;
+  if constexpr (C::V8) {
+    const int gg = lane >> 2, j = lane & 3;
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = key0 + 2 * j + (i & 1) + 8 * (i >> 1);
+      w[i] = lds32(v_base + C::VL::at(r, 2 * q + (gg >> 2)) + (gg & 3) * 4);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t lo = __byte_perm(w[2 * h], w[2 * h + 1], 0x5140), hi = __byte_perm(w[2 * h], w[2 * h + 1], 0x7362);
+      b[0][h] = e4m3x2_to_f16x2(lo & 0xffffu);
+      b[1][h] = e4m3x2_to_f16x2(lo >> 16);
+      b[2][h] = e4m3x2_to_f16x2(hi & 0xffffu);
+      b[3][h] = e4m3x2_to_f16x2(hi >> 16);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t r[4];
+      const int row = key0 + (lane & 7) + ((lane >> 3) & 1) * 8;
+      ldsm4t(r, v_base + C::VL::at(row, 4 * q + 2 * i + (lane >> 4)));
+      b[2 * i][0] = r[0];
+      b[2 * i][1] = r[1];
+      b[2 * i + 1][0] = r[2];
+      b[2 * i + 1][1] = r[3];
+    }
+  }
+}
+
+// Whether a 16-bit pair holds an infinity or a NaN.
+template <bool F16>
+__device__ __forceinline__ bool not_finite(uint32_t x) {
+  constexpr uint32_t E = F16 ? 0x7c00u : 0x7f80u;
+  return (x & E) == E || ((x >> 16) & E) == E;
+}
+template <bool F16>
+__device__ __forceinline__ float half_of(uint32_t x, int hi) {
+  const uint32_t h = hi ? x >> 16 : x & 0xffffu;
+  if constexpr (F16) return __half2float(__ushort_as_half(static_cast<unsigned short>(h)));
+  return __uint_as_float(h << 16);
+}
+
+template <class C>
+__device__ void consume(const CacheAttnParams& p, uint8_t* ring, float* red, CaMisc<C::STAGES>* misc, const Waiter w) {
+  using namespace ptx;
+  constexpr int D = C::D, KS = D / 16, NQ = D / 32;
+  constexpr int GPW = kGroups / C::WN;  // 16-key groups of a slot per warp
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wm = warp % C::WM, wn = warp / C::WM;
+  const int gq = lane >> 2, j = lane & 3;
+  uint32_t it = 0;
+  bool ok = true;
+  Walk<C::PICKED> walk;
+  walk.start(p);
+  Seg g;
+  while (walk.next(p, g)) {
+    const float sfk = sf_of(p.sf_k, p.sf_k_kind, g.b * static_cast<int64_t>(p.c.Hkv) + g.hkv);
+    const float sfv = sf_of(p.sf_v, p.sf_v_kind, g.b * static_cast<int64_t>(p.c.Hkv) + g.hkv);
+    // Q fragments: rows gq and gq + 8 of this warp's 16.
+    uint32_t qf[KS][4];
+    float cs[2];
+    Row rows[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      rows[h] = row_of<C>(p, g, wm * 16 + gq + 8 * h);
+      const uint16_t* src = p.q + g.b * p.q_sb + rows[h].tok * p.q_ss + rows[h].head * p.q_sh;
+      const bool live = rows[h].tok >= 0;
+      cs[h] = p.scale_log2 * sfk;
+      if constexpr (C::K8) {
+        // The codes' contraction runs in F16 (which holds them exactly): a row
+        // of Q is first brought to [1, 2) by a power of two, so it is exact
+        // too, but for values 2^-14 of the row's largest and smaller, which
+        // keep an absolute error of 2^-25 of it.
+        uint32_t raw[KS][2];
+        float top = 0.f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const uint2 v = live ? __ldg(reinterpret_cast<const uint2*>(src + 16 * s + 4 * j)) : make_uint2(0u, 0u);
+          raw[s][0] = v.x;
+          raw[s][1] = v.y;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            top = fmaxf(top, fabsf(half_of<false>(raw[s][e], 0)));
+            top = fmaxf(top, fabsf(half_of<false>(raw[s][e], 1)));
+          }
+        }
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+        int ex = static_cast<int>((__float_as_uint(top) >> 23) & 0xffu);
+        ex = (ex == 0 || ex == 255) ? 127 : min(ex, 253);  // zero rows and infinities as they are
+        const float down = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
+        cs[h] *= __uint_as_float(static_cast<uint32_t>(ex) << 23);
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            qf[s][h + 2 * e] = pack_f16x2(half_of<false>(raw[s][e], 0) * down, half_of<false>(raw[s][e], 1) * down);
+      } else {
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            qf[s][h + 2 * e] =
+                live ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * s + 8 * e + 2 * j)) : 0u;
+      }
+    }
+    float acc[NQ * 4][4];
+#pragma unroll
+    for (int i = 0; i < NQ * 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+    for (int u = g.t0; u < g.t1 && ok; ++u) {
+      const int s = it % C::STAGES;
+      ok = __all_sync(kFull, w.wait(smem_addr(&misc->full[s]), (it / C::STAGES) & 1));
+      if (!ok) break;
+      ++it;
+      const uint32_t k_base = smem_addr(ring + s * C::SLOT), v_base = k_base + C::KL::BYTES;
+      int valid[GPW], pos[GPW];
+      bool plain = true, any = false;  // every key of the warp's groups is seen by every row / some key exists
+#pragma unroll
+      for (int i = 0; i < GPW; ++i) {
+        valid[i] = misc->meta[s].valid[wn * GPW + i];
+        pos[i] = misc->meta[s].pos[wn * GPW + i];
+        any = any || valid[i] > 0;
+        plain = plain && valid[i] == 16 && pos[i] + 16 <= g.ctx;
+      }
+      if (any) {
+        // S = Q K^T, 16 rows x 16 keys per group.
+        float sc[GPW * 2][4];
+#pragma unroll
+        for (int i = 0; i < GPW * 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[i][e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < GPW; ++i) {
+          const int row = (wn * GPW + i) * 16 + (lane & 7) + (lane >> 4) * 8;
+          if constexpr (C::K8) {
+#pragma unroll
+            for (int s2 = 0; s2 < KS / 2; ++s2) {
+              uint32_t r[4];
+              ldsm4(r, k_base + C::KL::at(row, 2 * s2 + ((lane >> 3) & 1)));
+#pragma unroll
+              for (int e = 0; e < 4; ++e)  // e: which 16 columns (bit 0), which 8 keys (bit 1)
+                mma_f16(sc[2 * i + (e >> 1)], qf[2 * s2 + (e & 1)], e4m3x2_to_f16x2(r[e] & 0xffffu),
+                        e4m3x2_to_f16x2(r[e] >> 16));
+            }
+          } else {
+#pragma unroll
+            for (int s2 = 0; s2 < KS; ++s2) {
+              uint32_t r[4];
+              ldsm4(r, k_base + C::KL::at(row, 2 * s2 + ((lane >> 3) & 1)));
+              mma_bf16(sc[2 * i], qf[s2], r[0], r[1]);
+              mma_bf16(sc[2 * i + 1], qf[s2], r[2], r[3]);
+            }
+          }
+        }
+        if (!plain) {  // hide keys: past the end, or nodes this row does not see
+#pragma unroll
+          for (int i = 0; i < GPW * 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int k = (i & 1) * 8 + 2 * j + (e & 1);  // key inside the group
+              bool see = k < valid[i >> 1];
+              if constexpr (!C::PICKED) {
+                const int node = pos[i >> 1] + k - g.ctx;
+                const int tok = rows[e >> 1].tok;
+                if (see && node >= 0)
+                  see = tok >= 0 && (p.mask == nullptr
+                                         ? node <= tok
+                                         : p.mask[g.b * p.mask_sb + static_cast<int64_t>(tok) * p.c.T + node] != 0);
+              }
+              if (!see) sc[i][e] = -INFINITY;
+            }
+        }
+        // Running maximum, exponentials and row sums.
+        float mb[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < GPW * 2; ++i) mx = fmaxf(mx, fmaxf(sc[i][2 * h], sc[i][2 * h + 1]));
+          mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+          const float mn = fmaxf(m[h], mx * cs[h]);
+          const bool up = mn > m[h];
+          if (__any_sync(kFull, up)) {
+            const float f = up ? ex2(m[h] - mn) : 1.f;
+            m[h] = mn;
+            l[h] *= f;
+#pragma unroll
+            for (int i = 0; i < NQ * 4; ++i) {
+              acc[i][2 * h] *= f;
+              acc[i][2 * h + 1] *= f;
+            }
+          }
+          mb[h] = m[h] == -INFINITY ? 0.f : m[h];
+        }
+        uint32_t pf[GPW][4];
+        uint32_t seen = 0;  // not plain: bit 4 i + e of sc[i][e]
+#pragma unroll
+        for (int i = 0; i < GPW * 2; ++i) {
+          float e4[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (!plain && GPW <= 4 && sc[i][e] != -INFINITY) seen |= 1u << (4 * i + e);
+            e4[e] = ex2(fmaf(sc[i][e], cs[e >> 1], -mb[e >> 1]));
+            l[e >> 1] += e4[e];
+          }
+          pf[i >> 1][(i & 1) * 2] = pack_p<C>(e4[0], e4[1]);
+          pf[i >> 1][(i & 1) * 2 + 1] = pack_p<C>(e4[2], e4[3]);
+        }
+        // O += P V.
+#pragma unroll
+        for (int i = 0; i < GPW; ++i) {
+          if (!plain && valid[i] <= 0) continue;
+          const int key0 = (wn * GPW + i) * 16;
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            uint32_t b[4][2];
+            load_v<C>(b, v_base, key0, q, lane);
+            if (!plain) {
+              // Rows past the end hold anything: they count as zero. A node
+              // that some row does not see may hold infinities or NaN, which a
+              // zero weight would not stop: such a group adds key by key.
+              uint32_t keep[2];
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                keep[h] = (2 * j + 8 * h < valid[i] ? 0xffffu : 0u) | (2 * j + 1 + 8 * h < valid[i] ? 0xffff0000u : 0u);
+              bool odd = false;
+#pragma unroll
+              for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  b[n][h] &= keep[h];
+                  odd = odd || not_finite<C::V8>(b[n][h]);
+                }
+              if (__any_sync(kFull, odd)) {
+#pragma unroll 1
+                for (int k = 0; k < 16; ++k) {
+                  const int from = (lane & ~3) | ((k & 7) >> 1);
+                  const int bit = 4 * (2 * i + (k >> 3)) + (k & 1);
+                  const uint32_t sb = __shfl_sync(kFull, seen, from);
+                  // runtime-indexed registers: pick with selects
+                  uint32_t w0 = 0, w1 = 0;
+#pragma unroll
+                  for (int x = 0; x < 2; ++x) {
+                    const uint32_t a = __shfl_sync(kFull, pf[i][2 * x], from), c = __shfl_sync(kFull, pf[i][2 * x + 1], from);
+                    if ((k >> 3) == x) w0 = a, w1 = c;
+                  }
+                  const float p0 = half_of<C::V8>(w0, k & 1), p1 = half_of<C::V8>(w1, k & 1);
+                  const bool s0 = (sb >> bit) & 1u, s1 = (sb >> (bit + 2)) & 1u;
+#pragma unroll
+                  for (int n = 0; n < 4; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                      // column 2j + e of n-tile n: its key k sits in lane (2j + e) * 4 + (k & 7) / 2
+                      const uint32_t v0 = __shfl_sync(kFull, b[n][0], (2 * j + e) * 4 + ((k & 7) >> 1));
+                      const uint32_t v1 = __shfl_sync(kFull, b[n][1], (2 * j + e) * 4 + ((k & 7) >> 1));
+                      const float v = half_of<C::V8>(k < 8 ? v0 : v1, k & 1);
+                      if (s0) acc[4 * q + n][e] = fmaf(p0, v, acc[4 * q + n][e]);
+                      if (s1) acc[4 * q + n][2 + e] = fmaf(p1, v, acc[4 * q + n][2 + e]);
+                    }
+                }
+                continue;
+              }
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              if constexpr (C::V8) mma_f16(acc[4 * q + n], pf[i], b[n][0], b[n][1]);
+              else mma_bf16(acc[4 * q + n], pf[i], b[n][0], b[n][1]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&misc->empty[s]));
+    }
+
+    // Join the warps that shared the rows, and write O / l (or a partial).
+    float f[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(kFull, l[h], 1);
+      l[h] += __shfl_xor_sync(kFull, l[h], 2);
+    }
+    if (C::WN > 1) named_bar_sync(1, 128);  // the last item's (m, l) have been read
+    if (j == 0) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        misc->ml[warp][gq + 8 * h][0] = m[h];
+        misc->ml[warp][gq + 8 * h][1] = l[h];
+      }
+    }
+    if (C::WN > 1) named_bar_sync(1, 128);
+    else __syncwarp();
+    auto total = [&](int wmi, int r, float& M, float& L) {  // of row r of row group wmi
+      M = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < C::WN; ++x) M = fmaxf(M, misc->ml[x * C::WM + wmi][r][0]);
+      const float Mb = M == -INFINITY ? 0.f : M;
+      L = 0.f;
+#pragma unroll
+      for (int x = 0; x < C::WN; ++x) L += misc->ml[x * C::WM + wmi][r][1] * ex2(misc->ml[x * C::WM + wmi][r][0] - Mb);
+    };
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float M, L;
+      total(wm, gq + 8 * h, M, L);
+      f[h] = L != 0.f ? ex2(m[h] - (M == -INFINITY ? 0.f : M)) * (sfv / L) : 0.f;
+    }
+    const bool whole = g.t0 == 0 && g.t1 == g.nt;
+    const int64_t slot = 2ll * blockIdx.x + (g.t0 == 0 ? 1 : 0);
+    // Lanes that write: WN > 1: 8 per row over all 128 threads; else 8 per row of the warp.
+    const int tid = C::WN > 1 ? threadIdx.x : lane;
+    constexpr int PASS_ROWS = C::WN > 1 ? 16 : 4, PASSES = (C::WN > 1 ? C::ROWS : 16) / PASS_ROWS;
+#pragma unroll 1
+    for (int q = 0; q < NQ; ++q) {
+      float* mine = red + warp * 16 * C::RED_LD;
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int col = C::V8 ? 8 * j + 4 * (e & 1) + n : 8 * n + 2 * j + (e & 1);
+          float v = 0.f;
+#pragma unroll
+          for (int qq = 0; qq < NQ; ++qq)
+            if (qq == q) v = acc[4 * qq + n][e];
+          mine[(gq + 8 * (e >> 1)) * C::RED_LD + col] = v * f[e >> 1];
+        }
+      if (C::WN > 1) named_bar_sync(1, 128);
+      else __syncwarp();
+#pragma unroll
+      for (int ps = 0; ps < PASSES; ++ps) {
+        const int r = ps * PASS_ROWS + tid / 8, c4 = tid % 8;
+        const int wmi = C::WN > 1 ? r / 16 : wm, rr = r % 16;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int x = 0; x < C::WN; ++x) {
+          const float4 y =
+              *reinterpret_cast<const float4*>(red + ((x * C::WM + wmi) * 16 + rr) * C::RED_LD + 4 * c4);
+          v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
+        }
+        const int item_row = wmi * 16 + rr;
+        const Row ro = row_of<C>(p, g, item_row);
+        if (ro.tok < 0 || !ok) continue;
+        if (!whole) {
+          *reinterpret_cast<float4*>(p.part_o + (slot * C::ROWS + item_row) * D + 32 * q + 4 * c4) = v;
+        } else {
+          if (!C::PICKED && ro.tok >= g.nodes) v = make_float4(0.f, 0.f, 0.f, 0.f);
+          uint16_t* dst = p.o + g.b * p.o_sb + ro.tok * p.o_ss + ro.head * p.o_sh + 32 * q + 4 * c4;
+          *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        }
+        if (q == 0 && c4 == 0 && (!whole || p.lse != nullptr)) {
+          float M, L;
+          total(wmi, rr, M, L);
+          float lse = L != 0.f ? M + __log2f(L) : -INFINITY;
+          if (!whole) {
+            p.part_lse[slot * C::ROWS + item_row] = lse;
+          } else {
+            if (!C::PICKED && ro.tok >= g.nodes) lse = -INFINITY;
+            p.lse[(static_cast<int64_t>(g.b) * p.c.Hq + ro.head) * p.c.T + ro.tok] = lse * 0.69314718055994531f;
+          }
+        }
+      }
+      if (C::WN > 1) named_bar_sync(1, 128);
+      else __syncwarp();
+    }
+  }
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 2)
+    cache_attn_kernel(const __grid_constant__ CacheAttnParams p, const __grid_constant__ CUtensorMap tk,
+                      const __grid_constant__ CUtensorMap tv) {
+  using namespace ptx;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* red = reinterpret_cast<float*>(ring + C::STAGES * C::SLOT);
+  auto* misc = reinterpret_cast<CaMisc<C::STAGES>*>(ring + C::STAGES * C::SLOT + C::RED_BYTES);
+  static_assert(sizeof(CaMisc<C::STAGES>) <= 1024, "misc area");
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(smem_addr(&misc->full[s]), 1);
+      mbar_init(smem_addr(&misc->empty[s]), 4);
+    }
+    misc->abort = 0u;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  const Waiter w{&misc->abort, p.c.err, p.c.wait_cycles};
+  if (threadIdx.x >= 128) produce<C>(p, ring, misc, &tk, &tv, w);
+  else consume<C>(p, ring, red, misc, w);
+  __syncthreads();
+}
+
+// Merges the partials of items that several CTAs shared, and writes the rows
+// of items without any key. One warp per row.
+template <int D, bool PICKED>
+__global__ void __launch_bounds__(128) cache_merge_kernel(const __grid_constant__ CacheAttnParams p, int rows) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const int row = blockIdx.y * 4 + (threadIdx.x >> 5);
+  long long item = blockIdx.x;
+  const long long flat = item;
+  const int rt = static_cast<int>(item % p.row_tiles);
+  item /= p.row_tiles;
+  const int hkv = static_cast<int>(item % p.c.Hkv);
+  item /= p.c.Hkv;
+  int tok, head, b;
+  bool hidden = false;
+  long long first, last;  // CTAs that hold a partial of the item
+  if constexpr (PICKED) {
+    tok = static_cast<int>(item % p.c.T);
+    b = static_cast<int>(item / p.c.T);
+    const int i = rt * rows + row;
+    if (i >= p.c.G) return;
+    head = hkv * p.c.G + i;
+    first = flat * p.n_splits;
+    last = first + p.n_splits - 1;
+  } else {
+    b = static_cast<int>(item);
+    const int i = rt * rows + row;
+    tok = i / p.c.G;
+    if (tok >= p.c.T) return;
+    head = hkv * p.c.G + i - tok * p.c.G;
+    bool bad;
+    const SeqLens s = tree_lens(p.c, b, bad);
+    const int nt = tiles_of(s);
+    hidden = tok >= s.q || nt == 0;
+    const Share sh = tree_share(p, false);
+    const long long t0 = tree_tiles(p, b, false) * p.c.Hkv * p.row_tiles +
+                         static_cast<long long>(nt) * (hkv * p.row_tiles + rt);
+    first = t0 / sh.per;
+    last = nt > 0 ? (t0 + nt - 1) / sh.per : first;
+    if (nt > 0 && first == last) return;  // written whole
+  }
+  uint16_t* dst = p.o + b * p.o_sb + tok * p.o_ss + head * p.o_sh;
+  float* lse_out = p.lse == nullptr ? nullptr : p.lse + (static_cast<int64_t>(b) * p.c.Hq + head) * p.c.T + tok;
+  constexpr int V = D / 32;  // columns per lane
+  float acc[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.f;
+  float sum = 0.f, mx = -INFINITY;
+  if (!hidden) {
+    auto slot = [&](long long c) { return (2 * c + (c == first ? 1 : 0)) * rows + row; };
+    const int n = static_cast<int>(last - first + 1);
+    for (int k = lane; k < n; k += 32) mx = fmaxf(mx, p.part_lse[slot(first + k)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+    // A NaN partial must reach the row: fmaxf drops it, the weights keep it.
+    const float mb = mx == -INFINITY ? 0.f : mx;
+    for (int k0 = 0; k0 < n; k0 += 32) {
+      const float mine = k0 + lane < n ? p.part_lse[slot(first + k0 + lane)] : -INFINITY;
+      const float wgt = ptx::ex2(mine - mb);
+      const int m = min(32, n - k0);
+#pragma unroll 4
+      for (int k = 0; k < m; ++k) {
+        const float wk = __shfl_sync(kFull, wgt, k);
+        const float* src = p.part_o + slot(first + k0 + k) * D + lane * V;
+        sum += wk;
+        if (wk == 0.f) continue;  // a partial that saw no key
+        if constexpr (V == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          acc[0] = fmaf(wk, v.x, acc[0]);
+          acc[1] = fmaf(wk, v.y, acc[1]);
+          acc[2] = fmaf(wk, v.z, acc[2]);
+          acc[3] = fmaf(wk, v.w, acc[3]);
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(src);
+          acc[0] = fmaf(wk, v.x, acc[0]);
+          acc[1] = fmaf(wk, v.y, acc[1]);
+        }
+      }
+    }
+  }
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
+  if constexpr (V == 4)
+    *reinterpret_cast<uint2*>(dst + lane * 4) =
+        make_uint2(ptx::pack_bf16x2(acc[0] * inv, acc[1] * inv), ptx::pack_bf16x2(acc[2] * inv, acc[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(dst + lane * 2) = ptx::pack_bf16x2(acc[0] * inv, acc[1] * inv);
+  if (lse_out != nullptr && lane == 0)
+    *lse_out = sum != 0.f ? (mx + __log2f(sum)) * 0.69314718055994531f : -INFINITY;
+}
+
+template <class C>
+cudaError_t launch_cfg(const CacheAttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+  auto kern = cache_attn_kernel<C>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  kern<<<p.n_ctas, C::THREADS, C::SMEM, s>>>(p, tk, tv);
+  return cudaGetLastError();
+}
+
+template <int D, bool K8, bool V8, bool PICKED>
+cudaError_t launch_rows(const CacheAttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+  switch (cache_attn_rows(PICKED ? p.c.G : p.c.G * p.c.T)) {
+    case 16: return launch_cfg<CaCfg<D, K8, V8, 1, PICKED>>(p, tk, tv, s);
+    case 32: return launch_cfg<CaCfg<D, K8, V8, 2, PICKED>>(p, tk, tv, s);
+    default: return launch_cfg<CaCfg<D, K8, V8, 4, PICKED>>(p, tk, tv, s);
+  }
+}
+
+template <int D, bool PICKED>
+cudaError_t launch_types(bool k8, bool v8, const CacheAttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                         cudaStream_t s) {
+  if (k8) return launch_rows<D, true, true, PICKED>(p, tk, tv, s);
+  return v8 ? launch_rows<D, false, true, PICKED>(p, tk, tv, s) : launch_rows<D, false, false, PICKED>(p, tk, tv, s);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_attn(int D, bool k8, bool v8, const CacheAttnParams& p, const CUtensorMap& tk,
+                              const CUtensorMap& tv, cudaStream_t s) {
+  if (p.blocks != nullptr)
+    return D == 64 ? launch_types<64, true>(k8, v8, p, tk, tv, s) : launch_types<128, true>(k8, v8, p, tk, tv, s);
+  return D == 64 ? launch_types<64, false>(k8, v8, p, tk, tv, s) : launch_types<128, false>(k8, v8, p, tk, tv, s);
+}
+
+cudaError_t launch_cache_merge(int D, const CacheAttnParams& p, cudaStream_t s) {
+  const bool picked = p.blocks != nullptr;
+  const int rows = cache_attn_rows(picked ? p.c.G : p.c.G * p.c.T);
+  const long long items = static_cast<long long>(p.c.B) * (picked ? p.c.T : 1) * p.c.Hkv * p.row_tiles;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(items), rows / 4);
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  // Set up while the attention grid still runs (the kernel waits for its end).
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (picked)
+    return D == 64 ? cudaLaunchKernelEx(&cfg, cache_merge_kernel<64, true>, p, rows)
+                   : cudaLaunchKernelEx(&cfg, cache_merge_kernel<128, true>, p, rows);
+  return D == 64 ? cudaLaunchKernelEx(&cfg, cache_merge_kernel<64, false>, p, rows)
+                 : cudaLaunchKernelEx(&cfg, cache_merge_kernel<128, false>, p, rows);
+}
+
+}  // namespace fmha

@@ -11,6 +11,7 @@ factor is given as ``Scale(tensor, kind, rows_per_block)`` with ``kind`` one
 of "per_tensor", "per_head", "per_token_block", "per_channel".
 """
 
+import contextlib
 import ctypes
 import math
 import os
@@ -86,6 +87,13 @@ def load_library(path=None):
     lib.fmha_decode_workspace_bytes.restype = sz
     lib.fmha_decode_num_splits.argtypes = [ctypes.POINTER(_Args), i32]
     lib.fmha_decode_num_splits.restype = i32
+    cache = ctypes.POINTER(_CacheArgs)
+    lib.fmha_fwd_tree.argtypes = [cache, vp, i64, vp, sz, vp]
+    lib.fmha_fwd_tree_workspace_bytes.argtypes = [cache]
+    lib.fmha_fwd_selected.argtypes = [cache, vp, i32, i32, vp, sz, vp]
+    lib.fmha_fwd_selected_workspace_bytes.argtypes = [cache, i32, i32]
+    for f in ("fmha_fwd_tree_workspace_bytes", "fmha_fwd_selected_workspace_bytes"):
+        getattr(lib, f).restype = sz
     lib.fmha_status_string.argtypes = [ctypes.c_int]
     lib.fmha_status_string.restype = ctypes.c_char_p
     lib.fmha_last_error_message.restype = ctypes.c_char_p
@@ -375,3 +383,166 @@ def get_device_error(stream=None):
 
 def set_wait_timeout_cycles(cycles):
     load_library().fmha_set_wait_timeout_cycles(int(cycles))
+
+
+# ------------------------------------------------- operators over a ragged cache
+class _CacheArgs(ctypes.Structure):
+    _fields_ = [("q", _Tensor), ("k", _Tensor), ("v", _Tensor), ("o", _Tensor), ("sf_k", _Sf), ("sf_v", _Sf),
+                ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("capacity", ctypes.c_int32),
+                ("lens", ctypes.c_void_p), ("q_lens", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("max_pages_per_seq", ctypes.c_int32),
+                ("softmax_scale", ctypes.c_float), ("lse", ctypes.c_void_p)]
+
+
+@contextlib.contextmanager
+def _launch(stream, *tensors):
+    """Makes the tensors' device current, and `stream` (None: that device's current stream) the stream that
+    outputs and workspaces allocated inside belong to. Yields the stream handle."""
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) != 1 or next(iter(devices)).type != "cuda":
+        raise ValueError(f"all tensors must be on one CUDA device, got {sorted(map(str, devices))}")
+    device = devices.pop()
+    with torch.cuda.device(device):
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+        elif stream.device != device:
+            raise ValueError(f"stream of {stream.device} for tensors of {device}")
+        with torch.cuda.stream(stream):
+            yield ctypes.c_void_p(stream.cuda_stream)
+
+
+def _ints(t, shape, what):
+    """Checks an int32 tensor's shape and contiguity; returns its address (None for None)."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 tensor of shape {list(shape)}")
+    return t.data_ptr()
+
+
+def _floats(t, shape, what):
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous float32 tensor of shape {list(shape)}")
+    return t.data_ptr()
+
+
+def _cache_sf(s, B, Hkv, what):
+    if s is not None and s.kind == "per_head" and tuple(s.tensor.shape) != (B, Hkv):
+        raise ValueError(f"{what}: per-head scales must have shape [{B}, {Hkv}]")
+    if s is not None and s.tensor.numel() == 0:
+        raise ValueError(f"{what}: empty scale tensor")
+    return _sf(s)
+
+
+def _cache_args(k, lens, page_table, q=None, v=None, out=None, q_lens=None, sf_k=None, sf_v=None,
+                softmax_scale=None, lse=None):
+    """_CacheArgs of k (and v) [B, S, Hkv, D], or pools [pages, page_size, Hkv, D] with a page table [B, max_pages]."""
+    a = _CacheArgs()
+    a.k = _tensor(k)
+    a.Hkv, a.D = k.shape[2], k.shape[3]
+    if page_table is not None:
+        if page_table.dim() != 2:
+            raise ValueError("page_table must be contiguous int32 [B, max_pages_per_seq]")
+        a.B = page_table.shape[0]
+        a.page_table = _ints(page_table, page_table.shape, "page_table")
+        a.num_pages, a.page_size, a.max_pages_per_seq = k.shape[0], k.shape[1], page_table.shape[1]
+        a.capacity = a.max_pages_per_seq * a.page_size
+    else:
+        a.B, a.capacity = k.shape[0], k.shape[1]
+    if v is not None:
+        if v.shape != k.shape:
+            raise ValueError(f"k {list(k.shape)} and v {list(v.shape)} differ in shape")
+        a.v = _tensor(v)
+    a.lens = _ints(lens, (a.B,), "lens")
+    a.q_lens = _ints(q_lens, (a.B,), "q_lens")
+    a.sf_k, a.sf_v = _cache_sf(sf_k, a.B, a.Hkv, "sf_k"), _cache_sf(sf_v, a.B, a.Hkv, "sf_v")
+    if q is not None:
+        a.q = _tensor(q)
+        if q.shape[0] != a.B or q.shape[3] != a.D:
+            raise ValueError(f"q {list(q.shape)} does not fit a cache of {a.B} sequences with head dim {a.D}")
+        a.T, a.Hq = q.shape[1], q.shape[2]
+        a.lse = _floats(lse, (a.B, a.Hq, a.T), "lse")
+    if out is not None:
+        if out.shape != q.shape:
+            raise ValueError(f"out {list(out.shape)} differs from q {list(q.shape)} in shape")
+        a.o = _tensor(out)
+    a.softmax_scale = float(softmax_scale) if softmax_scale else 0.0
+    return a
+
+
+def _scratch(workspace, need, device):
+    """(address, bytes) of the caller's workspace, or of one allocated here."""
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    elif workspace.device != device:
+        raise ValueError(f"workspace on {workspace.device}, tensors on {device}")
+    return (workspace, None, 0) if workspace is None else (
+        workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+
+
+def _sf_tensors(*scales):
+    return [s.tensor for s in scales if s is not None]
+
+
+def fmha_fwd_tree(q, k, v, ctx_lens, tree_mask=None, tree_lens=None, page_table=None, workspace=None, out=None,
+                  sf_k=None, sf_v=None, softmax_scale=None, lse=None, stream=None):
+    """Attention of a tree of drafted tokens over a ragged cache. Returns O (BF16 [B, T, Hq, D]).
+
+    q: BF16 [B, T, Hq, D], the drafted nodes. k / v: [B, S, Hkv, D], or page pools
+    [num_pages, page_size, Hkv, D] with page_table int32 [B, max_pages]; BF16 or E4M3 (with sf_k / sf_v).
+    ctx_lens: int32 [B], tokens before the tree; node j of sequence b stands at position ctx_lens[b] + j.
+    tree_lens: int32 [B], nodes in use (None: T). tree_mask: uint8 [B or 1, T, T], nonzero where node i (row)
+    sees node j; None: a chain (node i sees nodes 0..i), so T = 1 is an ordinary decoding step of a ragged batch.
+    lse (optional): contiguous fp32 [B, Hq, T]. Rows that see no key give O = 0, lse = -inf."""
+    a = _cache_args(k, ctx_lens, page_table, q=q, v=v, out=out, q_lens=tree_lens, sf_k=sf_k, sf_v=sf_v,
+                    softmax_scale=softmax_scale, lse=lse)
+    mask_sb = 0
+    if tree_mask is not None:
+        T = q.shape[1]
+        if (tree_mask.dtype != torch.uint8 or tree_mask.dim() != 3 or tree_mask.shape[0] not in (1, a.B)
+                or tuple(tree_mask.shape[1:]) != (T, T) or (T > 1 and (tree_mask.stride(2) != 1 or tree_mask.stride(1) != T))):
+            raise ValueError(f"tree_mask must be uint8 [{a.B} or 1, {T}, {T}] with contiguous rows")
+        mask_sb = tree_mask.stride(0) if tree_mask.shape[0] > 1 else 0
+    lib = load_library()
+    with _launch(stream, q, k, v, ctx_lens, tree_mask, tree_lens, page_table, out, lse, *_sf_tensors(sf_k, sf_v)) as s:
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+            a.o = _tensor(out)
+        need = lib.fmha_fwd_tree_workspace_bytes(ctypes.byref(a))
+        workspace, ptr, size = _scratch(workspace, need, q.device)
+        _check(lib.fmha_fwd_tree(ctypes.byref(a), tree_mask.data_ptr() if tree_mask is not None else None, mask_sb,
+                                 ptr, size, s))
+    return out
+
+
+def tree_workspace_bytes(q, k, page_table=None):
+    """Workspace bytes fmha_fwd_tree needs for these shapes (host only)."""
+    lens = torch.empty(q.shape[0], dtype=torch.int32)
+    return load_library().fmha_fwd_tree_workspace_bytes(ctypes.byref(_cache_args(k, lens, page_table, q=q)))
+
+
+def fmha_fwd_selected(q, k, v, blocks, lens, block, q_lens=None, page_table=None, workspace=None, out=None,
+                      sf_k=None, sf_v=None, softmax_scale=None, lse=None, stream=None):
+    """Attention over the key blocks picked for each query token. Returns O (BF16 [B, T, Hq, D]).
+
+    blocks: contiguous int32 [B, T, Hkv, top], ids of the `block`-key blocks (16, 32, 64 or 128) that query token
+    t reads in KV head h; negative: none (``select_blocks`` makes them). lens: int32 [B], tokens in the cache;
+    the q_lens[b] (None: T) query tokens are its last ones, and each sees keys up to its own position."""
+    a = _cache_args(k, lens, page_table, q=q, v=v, out=out, q_lens=q_lens, sf_k=sf_k, sf_v=sf_v,
+                    softmax_scale=softmax_scale, lse=lse)
+    if blocks.dim() != 4:
+        raise ValueError("blocks must be a contiguous int32 [B, T, Hkv, top] tensor")
+    ids = _ints(blocks, (a.B, a.T, a.Hkv, blocks.shape[3]), "blocks")
+    top = blocks.shape[3]
+    lib = load_library()
+    with _launch(stream, q, k, v, blocks, lens, q_lens, page_table, out, lse, *_sf_tensors(sf_k, sf_v)) as s:
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+            a.o = _tensor(out)
+        need = lib.fmha_fwd_selected_workspace_bytes(ctypes.byref(a), top, int(block))
+        workspace, ptr, size = _scratch(workspace, need, q.device)
+        _check(lib.fmha_fwd_selected(ctypes.byref(a), ids, top, int(block), ptr, size, s))
+    return out
