@@ -401,6 +401,88 @@ fmha_status fmha_fwd_selected(const fmha_cache_args* args, const int32_t* blocks
                               void* workspace, size_t workspace_bytes, struct CUstream_st* stream);
 size_t fmha_fwd_selected_workspace_bytes(const fmha_cache_args* args, int32_t top, int32_t block);
 
+/* Bounds of each block of cached keys, for fmha_select_blocks: the smallest
+ * and the largest key of block j, per channel, over the keys the block has.
+ *   Reads k (of args: k, B, Hkv, D, capacity, lens = tokens in the cache, the
+ *     page table). The codes of E4M3 keys are taken as they are (a positive
+ *     scale moves no pick). Keys must be finite.
+ *   bounds: BF16 [B, Hkv, n_blocks, 2, D] contiguous, device, 16-byte aligned:
+ *     minima at [..., 0, :], maxima at [..., 1, :] (exact: no value is
+ *     rounded). Blocks past a sequence's end are left as they were.
+ *   block: 16, 32, 64 or 128. start (nullable): int32 [B], device: blocks that
+ *     end at or before position start[b] are left as they were, so a decoding
+ *     step refreshes the last block only.                                   */
+fmha_status fmha_key_bounds(const fmha_cache_args* args, void* bounds, int32_t n_blocks, int32_t block,
+                            const int32_t* start, struct CUstream_st* stream);
+
+/* Picks the blocks of keys that each query attends to, by the score
+ *   score_j = sum over the query heads h of the KV head of
+ *             sum_d max(q_hd * min_jd, q_hd * max_jd)
+ * (the largest product with q_h that a key inside block j's bounds could have,
+ * summed over the heads), in 64 bits. Of the blocks up to the query's own
+ * position the first sink_blocks and the last recent_blocks are picked first,
+ * then the best scores, until `top` are; ties go to the lowest block.
+ *   Reads q (of args: q, B, T, Hq, Hkv, D, lens, q_lens; positions as in
+ *     fmha_fwd_selected) and bounds (as fmha_key_bounds writes them).
+ *   q_tile 1: every query token picks; `picked` is int32 [B, T, Hkv, top]:
+ *     ascending block ids, then -1 (fmha_fwd_selected reads it).
+ *   q_tile 128 (with block 128): tiles of 128 query tokens pick together, by
+ *     the sum of their scores and up to the position of the tile's last token;
+ *     `picked` is the uint8 block mask [B, Hkv, ceil(T/128), n_blocks] that
+ *     fmha_fwd_block_sparse and fmha_fwd_paged take.
+ *   n_blocks <= 16384.                                                      */
+fmha_status fmha_select_blocks(const fmha_cache_args* args, const void* bounds, int32_t n_blocks, int32_t block,
+                               int32_t top, int32_t sink_blocks, int32_t recent_blocks, int32_t q_tile,
+                               void* picked, struct CUstream_st* stream);
+
+/* Attention weight that each cached key gathers over the query tokens:
+ *   w[b, h, s] (+)= sum over query tokens t and the query heads g of KV head h
+ *                   of exp(softmax_scale * q_tg . k_s - lse[b, g, t])
+ * over the keys in sight of t (causal: up to its own position, as in
+ * fmha_fwd_selected; else all lens[b] keys). args->lse is read: the
+ * log-sum-exp that an attention call on the same q and keys wrote.
+ *   Reads q, k, lse, lens, q_lens and sf_k of args.
+ *   weights: fp32 [B, Hkv, n_weights] contiguous, device; accumulate != 0 adds,
+ *     0 overwrites. Entries at or past lens[b] are left as they were;
+ *     lens[b] <= n_weights. The same inputs give the same bits.             */
+fmha_status fmha_key_weights(const fmha_cache_args* args, float* weights, int32_t n_weights, int32_t causal,
+                             int32_t accumulate, struct CUstream_st* stream);
+
+/* The keys of each (sequence, KV head) that stay under a budget. With
+ * n = lens[b] > budget: the first `sinks`, the last `recent`, and of the others
+ * the budget - sinks - recent with the largest weights (ties to the lowest
+ * position; a NaN weighs less than anything). With n <= budget: all of them.
+ *   Reads B, Hkv and lens of args, and capacity (0: n_weights).
+ *   weights: as above. keep: int32 [B, Hkv, budget]: ascending positions, then
+ *     -1. counts: int32 [B]: min(lens[b], budget), the sequence's new length.
+ *   0 <= sinks, 0 <= recent, sinks + recent <= budget, budget >= 1.         */
+fmha_status fmha_evict_select(const fmha_cache_args* args, const float* weights, int32_t n_weights, int32_t budget,
+                              int32_t sinks, int32_t recent, int32_t* keep, int32_t* counts,
+                              struct CUstream_st* stream);
+
+/* Moves the kept rows of a cache together: row i < counts[b] of KV head h goes
+ * to position dst_start[b] + i (dst_start NULL: i) from position keep[b, h, i],
+ * in K, V and (where given) the weights. After fmha_evict_select this shrinks
+ * a cache; with dst_start = the context's length and keep = the positions of
+ * an accepted path it commits a drafted tree.
+ *   Reads k, v, B, Hkv, D, capacity, page table of args; any K / V dtypes.
+ *   out: NULL: inside the same cache. Positions must then ascend with i and
+ *     keep[b, h, i] >= dst_start[b] + i, and no page may belong to two
+ *     sequences. Else the k, v, page table and capacity of another cache, not
+ *     overlapping the first, with the same dtypes, B, Hkv and D; any order.
+ *   keep: int32, element (b, h, i) at keep[b*keep_stride_b + h*keep_stride_h +
+ *     i], n_keep of them per head; strides may be 0. counts[b] <= n_keep.
+ *   weights / weights_out (both or neither; the same pointer exactly when out
+ *     is NULL): fp32 [B, Hkv, n_weights] / [B, Hkv, n_weights_out]; entries of
+ *     weights_out past the moved ones become 0.
+ * Rows that are not written to keep what they held. A position out of range,
+ * or (out NULL) out of order, is left out and reported as
+ * FMHA_ERR_DEVICE_INDEX.                                                     */
+fmha_status fmha_cache_compact(const fmha_cache_args* args, const fmha_cache_args* out, const int32_t* keep,
+                               int64_t keep_stride_b, int64_t keep_stride_h, int32_t n_keep, const int32_t* counts,
+                               const int32_t* dst_start, const float* weights, int32_t n_weights, float* weights_out,
+                               int32_t n_weights_out, struct CUstream_st* stream);
+
 /* Workspace bytes fmha_fwd_decode needs for these args and num_splits
  * (0: a single split, or invalid sizes). Host only.                         */
 size_t fmha_decode_workspace_bytes(const fmha_args* args, int32_t num_splits);

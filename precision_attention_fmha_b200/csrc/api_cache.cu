@@ -158,6 +158,23 @@ fmha_status check_workspace(const void* ws, size_t have, size_t need) {
   return FMHA_OK;
 }
 
+fmha_status check_block(int block) {
+  if (block != 16 && block != 32 && block != 64 && block != 128)
+    return fail(FMHA_ERR_UNSUPPORTED, "block %d (supported: 16, 32, 64, 128)", block);
+  return FMHA_OK;
+}
+
+constexpr int kMaxPickBlocks = 16384;  // their 64-bit scores fit one CTA's shared memory
+// Query tokens from which fmha_key_weights runs on the tensor cores' 128-token tiles.
+constexpr int kManyQueries = 64;
+
+// CTAs that score the blocks of one item: enough to give every SM one, while each keeps at least 64 blocks.
+int pick_cluster(int64_t items, int n_blocks) {
+  int c = 1;
+  while (c < 8 && items * c < sm_count() && n_blocks / (2 * c) >= 64) c *= 2;
+  return c;
+}
+
 // Fills what the tree and the picked form share, with the TMA maps.
 fmha_status fill_attn(const fmha_cache_args* a, CacheAttnParams* p, bool* k8, bool* v8, int piece, CUtensorMap* tk,
                       CUtensorMap* tv) {
@@ -238,8 +255,8 @@ fmha_status fmha_fwd_selected(const fmha_cache_args* a, const int32_t* blocks, i
   if (a == nullptr) return fail(FMHA_ERR_INVALID_ARG, "args is NULL");
   if (!sizes_ok(a)) return fail(FMHA_ERR_INVALID_ARG, "negative size");
   if (a->B == 0 || a->T == 0 || a->Hq == 0) return ok_status();  // nothing to compute
-  if (block != 16 && block != 32 && block != 64 && block != 128)
-    return fail(FMHA_ERR_UNSUPPORTED, "block %d (supported: 16, 32, 64, 128)", block);
+  fmha_status st;
+  if ((st = check_block(block)) != FMHA_OK) return st;
   if (top <= 0 || static_cast<int64_t>(top) * block > INT32_MAX / 2)
     return fail(FMHA_ERR_INVALID_ARG, "top %d out of range", top);
   if (blocks == nullptr || (reinterpret_cast<uintptr_t>(blocks) & 3u))
@@ -247,7 +264,6 @@ fmha_status fmha_fwd_selected(const fmha_cache_args* a, const int32_t* blocks, i
   CacheAttnParams p;
   CUtensorMap tk, tv;
   bool k8, v8;
-  fmha_status st;
   if ((st = fill_attn(a, &p, &k8, &v8, block, &tk, &tv)) != FMHA_OK) return st;
   PickPlan t;
   if (!pick_plan(a, top, block, &t)) return fail(FMHA_ERR_UNSUPPORTED, "grid too large");
@@ -266,6 +282,248 @@ fmha_status fmha_fwd_selected(const fmha_cache_args* a, const int32_t* blocks, i
   cudaError_t e = launch_cache_attn(a->D, k8, v8, p, tk, tv, stream);
   if (e == cudaSuccess && t.n_splits > 1) e = launch_cache_merge(a->D, p, stream);
   if (e != cudaSuccess) return fail(FMHA_ERR_CUDA, "picked-block attention launch: %s", cudaGetErrorString(e));
+  return ok_status();
+}
+
+fmha_status fmha_key_bounds(const fmha_cache_args* a, void* bounds, int32_t n_blocks, int32_t block,
+                            const int32_t* start, cudaStream_t stream) {
+  if (a == nullptr) return fail(FMHA_ERR_INVALID_ARG, "args is NULL");
+  if (!sizes_ok(a) || n_blocks < 0) return fail(FMHA_ERR_INVALID_ARG, "negative size");
+  if (a->B == 0 || a->Hkv == 0 || n_blocks == 0) return ok_status();
+  fmha_status st;
+  if ((st = check_block(block)) != FMHA_OK) return st;
+  if (bounds == nullptr || !aligned16(bounds)) return fail(FMHA_ERR_INVALID_ARG, "bounds is NULL or not 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(start) & 3u) return fail(FMHA_ERR_INVALID_ARG, "start misaligned");
+  KeyBoundsParams p;
+  memset(&p, 0, sizeof(p));
+  bool k8, v8;
+  if ((st = check_cache(a, false, false, &p.c, &k8, &v8)) != FMHA_OK) return st;
+  if (static_cast<int64_t>(a->B) * a->Hkv * n_blocks >= (int64_t(1) << 33))
+    return fail(FMHA_ERR_UNSUPPORTED, "grid too large");
+  p.k = static_cast<const uint8_t*>(a->k.ptr);
+  p.k_sb = a->k.stride_b; p.k_ss = a->k.stride_s; p.k_sh = a->k.stride_h;
+  p.bounds = static_cast<uint16_t*>(bounds);
+  p.start = start;
+  p.n_blocks = n_blocks;
+  p.block_shift = log2_of(block);
+  cudaError_t e = launch_key_bounds(a->D, k8, p, stream);
+  if (e != cudaSuccess) return fail(FMHA_ERR_CUDA, "key bounds launch: %s", cudaGetErrorString(e));
+  return ok_status();
+}
+
+fmha_status fmha_select_blocks(const fmha_cache_args* a, const void* bounds, int32_t n_blocks, int32_t block,
+                               int32_t top, int32_t sink_blocks, int32_t recent_blocks, int32_t q_tile, void* picked,
+                               cudaStream_t stream) {
+  if (a == nullptr) return fail(FMHA_ERR_INVALID_ARG, "args is NULL");
+  if (!sizes_ok(a) || n_blocks < 0) return fail(FMHA_ERR_INVALID_ARG, "negative size");
+  if (a->B == 0 || a->T == 0 || a->Hq == 0) return ok_status();
+  fmha_status st;
+  if ((st = check_block(block)) != FMHA_OK) return st;
+  if (top <= 0) return fail(FMHA_ERR_INVALID_ARG, "top must be positive");
+  if (sink_blocks < 0 || recent_blocks < 0) return fail(FMHA_ERR_INVALID_ARG, "negative sink_blocks or recent_blocks");
+  if (q_tile != 1 && q_tile != 128) return fail(FMHA_ERR_UNSUPPORTED, "q_tile %d (supported: 1, 128)", q_tile);
+  if (q_tile == 128 && block != 128) return fail(FMHA_ERR_UNSUPPORTED, "q_tile 128 needs blocks of 128 keys");
+  if (n_blocks > kMaxPickBlocks) return fail(FMHA_ERR_UNSUPPORTED, "%d blocks (supported: up to %d)", n_blocks, kMaxPickBlocks);
+  if (a->D != 64 && a->D != 128) return fail(FMHA_ERR_UNSUPPORTED, "head dim %d (supported: 64, 128)", a->D);
+  if (a->Hkv == 0 || a->Hq % a->Hkv != 0)
+    return fail(FMHA_ERR_INVALID_ARG, "Hq (%d) must be a multiple of Hkv (%d)", a->Hq, a->Hkv);
+  if (a->q.dtype != FMHA_BF16) return fail(FMHA_ERR_UNSUPPORTED, "q must be BF16");
+  if ((st = check_tensor(a->q, "q", a->B, a->T, a->Hq, a->D)) != FMHA_OK) return st;
+  if (n_blocks > 0 && (bounds == nullptr || !aligned16(bounds)))
+    return fail(FMHA_ERR_INVALID_ARG, "bounds is NULL or not 16-byte aligned");
+  if (picked == nullptr || (q_tile == 1 && (reinterpret_cast<uintptr_t>(picked) & 3u)))
+    return fail(FMHA_ERR_INVALID_ARG, "picked is NULL or misaligned");
+  if (a->lens == nullptr || (reinterpret_cast<uintptr_t>(a->lens) & 3u))
+    return fail(FMHA_ERR_INVALID_ARG, "lens is NULL or misaligned");
+  if (reinterpret_cast<uintptr_t>(a->q_lens) & 3u) return fail(FMHA_ERR_INVALID_ARG, "q_lens misaligned");
+  const int G = a->Hq / a->Hkv;
+  const int n_tiles = ceil_div(a->T, q_tile);
+  const int64_t items = static_cast<int64_t>(a->B) * n_tiles * a->Hkv;
+  if (items >= (int64_t(1) << 27) || static_cast<int64_t>(a->T) * G > INT32_MAX / 2)
+    return fail(FMHA_ERR_UNSUPPORTED, "grid too large");
+  SelectParams p;
+  memset(&p, 0, sizeof(p));
+  p.c.B = a->B; p.c.T = a->T; p.c.Hq = a->Hq; p.c.Hkv = a->Hkv; p.c.G = G;
+  p.c.capacity = n_blocks * block;
+  p.c.lens = a->lens;
+  p.c.q_lens = a->q_lens;
+  cudaError_t e;
+  p.c.err = device_error_word(&e);
+  if (p.c.err == nullptr) return fail(FMHA_ERR_CUDA, "device error word: %s", cudaGetErrorString(e));
+  p.q = static_cast<const uint16_t*>(a->q.ptr);
+  p.q_sb = a->q.stride_b; p.q_ss = a->q.stride_s; p.q_sh = a->q.stride_h;
+  p.bounds = static_cast<const uint16_t*>(bounds);
+  p.n_blocks = n_blocks;
+  p.block_shift = log2_of(block);
+  p.top = top; p.sinks = sink_blocks; p.recent = recent_blocks;
+  p.q_tile = q_tile;
+  p.n_tiles = n_tiles;
+  p.cluster = pick_cluster(items, n_blocks);
+  if (q_tile == 1) p.list = static_cast<int32_t*>(picked);
+  else p.mask = static_cast<uint8_t*>(picked);
+  e = launch_select_blocks(a->D, p, stream);
+  if (e != cudaSuccess) return fail(FMHA_ERR_CUDA, "block selection launch: %s", cudaGetErrorString(e));
+  return ok_status();
+}
+
+fmha_status fmha_key_weights(const fmha_cache_args* a, float* weights, int32_t n_weights, int32_t causal,
+                             int32_t accumulate, cudaStream_t stream) {
+  if (a == nullptr) return fail(FMHA_ERR_INVALID_ARG, "args is NULL");
+  if (!sizes_ok(a) || n_weights < 0) return fail(FMHA_ERR_INVALID_ARG, "negative size");
+  if (a->B == 0 || a->T == 0 || a->Hq == 0 || n_weights == 0) return ok_status();
+  if (weights == nullptr || (reinterpret_cast<uintptr_t>(weights) & 3u))
+    return fail(FMHA_ERR_INVALID_ARG, "weights is NULL or misaligned");
+  if (a->lse == nullptr) return fail(FMHA_ERR_INVALID_ARG, "lse is NULL");
+  KeyWeightsParams p;
+  memset(&p, 0, sizeof(p));
+  bool k8, v8;
+  fmha_status st;
+  if ((st = check_cache(a, true, false, &p.c, &k8, &v8)) != FMHA_OK) return st;
+  if (p.c.capacity == 0) return ok_status();  // no key
+  p.q = static_cast<const uint16_t*>(a->q.ptr);
+  p.q_sb = a->q.stride_b; p.q_ss = a->q.stride_s; p.q_sh = a->q.stride_h;
+  p.k = static_cast<const uint8_t*>(a->k.ptr);
+  p.k_sb = a->k.stride_b; p.k_ss = a->k.stride_s; p.k_sh = a->k.stride_h;
+  p.lse = a->lse;
+  p.weights = weights;
+  p.n_weights = n_weights;
+  p.causal = causal != 0;
+  p.accumulate = accumulate != 0;
+  const float scale = a->softmax_scale > 0.f ? a->softmax_scale : 1.0f / std::sqrt(float(a->D));
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.sf_k = a->sf_k.ptr; p.sf_k_kind = a->sf_k.kind;
+  const int64_t heads = static_cast<int64_t>(a->B) * a->Hkv;
+  cudaError_t e;
+  CUtensorMap m;
+  if (a->T >= kManyQueries) {
+    const int64_t n = heads * ceil_div(std::min(p.c.capacity, n_weights), 128);
+    if (n >= (int64_t(1) << 31)) return fail(FMHA_ERR_UNSUPPORTED, "grid too large");
+    p.n_ctas = static_cast<int>(n);
+    const uint64_t dims[4] = {uint64_t(a->D), uint64_t(a->Hq), uint64_t(a->T), uint64_t(a->B)};
+    const int64_t strides[3] = {a->q.stride_h, a->q.stride_s, a->q.stride_b};
+    const uint32_t box[4] = {64, 1, 128, 1};
+    if ((st = make_map_n<4>(&m, a->q.ptr, 2, dims, strides, box, "q")) != FMHA_OK) return st;
+    e = launch_key_weights_many(a->D, k8, p, m, stream);
+  } else {
+    const int piece = p.c.page_table != nullptr ? std::min(kTile, a->page_size) : kTile;
+    if ((st = cache_map(&m, a, p.c, a->k, k8, piece, "k")) != FMHA_OK) return st;
+    p.piece_shift = log2_of(piece);
+    p.row_tiles = 1;
+    p.min_tiles = 1;
+    const int64_t tiles = heads * ceil_div(p.c.capacity, kTile);
+    p.n_ctas = static_cast<int>(std::min<int64_t>(2 * sm_count(), tiles));
+    if (tiles / p.n_ctas >= (int64_t(1) << 30)) return fail(FMHA_ERR_UNSUPPORTED, "grid too large");
+    e = launch_key_weights_few(a->D, k8, p, m, stream);
+  }
+  if (e != cudaSuccess) return fail(FMHA_ERR_CUDA, "key weights launch: %s", cudaGetErrorString(e));
+  return ok_status();
+}
+
+fmha_status fmha_evict_select(const fmha_cache_args* a, const float* weights, int32_t n_weights, int32_t budget,
+                              int32_t sinks, int32_t recent, int32_t* keep, int32_t* counts, cudaStream_t stream) {
+  if (a == nullptr) return fail(FMHA_ERR_INVALID_ARG, "args is NULL");
+  if (a->B < 0 || a->Hkv < 0 || n_weights < 0 || a->capacity < 0) return fail(FMHA_ERR_INVALID_ARG, "negative size");
+  if (budget < 1 || sinks < 0 || recent < 0 || static_cast<int64_t>(sinks) + recent > budget)
+    return fail(FMHA_ERR_INVALID_ARG, "budget %d must be positive and hold sinks %d + recent %d", budget, sinks, recent);
+  if (a->B == 0 || a->Hkv == 0) return ok_status();
+  if (a->lens == nullptr || (reinterpret_cast<uintptr_t>(a->lens) & 3u))
+    return fail(FMHA_ERR_INVALID_ARG, "lens is NULL or misaligned");
+  if (n_weights > 0 && (weights == nullptr || (reinterpret_cast<uintptr_t>(weights) & 3u)))
+    return fail(FMHA_ERR_INVALID_ARG, "weights is NULL or misaligned");
+  if (keep == nullptr || counts == nullptr || ((reinterpret_cast<uintptr_t>(keep) | reinterpret_cast<uintptr_t>(counts)) & 3u))
+    return fail(FMHA_ERR_INVALID_ARG, "keep or counts is NULL or misaligned");
+  if (static_cast<int64_t>(a->B) * a->Hkv >= (int64_t(1) << 31)) return fail(FMHA_ERR_UNSUPPORTED, "grid too large");
+  if (n_weights > INT32_MAX / 2 || budget > INT32_MAX / 2)
+    return fail(FMHA_ERR_UNSUPPORTED, "more than 2^30 tokens per sequence");
+  EvictParams p;
+  memset(&p, 0, sizeof(p));
+  p.c.B = a->B; p.c.Hkv = a->Hkv;
+  p.c.capacity = a->capacity > 0 ? a->capacity : n_weights;
+  p.c.lens = a->lens;
+  cudaError_t e;
+  p.c.err = device_error_word(&e);
+  if (p.c.err == nullptr) return fail(FMHA_ERR_CUDA, "device error word: %s", cudaGetErrorString(e));
+  p.weights = weights;
+  p.n_weights = n_weights;
+  p.budget = budget; p.sinks = sinks; p.recent = recent;
+  p.keep = keep;
+  p.counts = counts;
+  e = launch_evict_select(p, stream);
+  if (e != cudaSuccess) return fail(FMHA_ERR_CUDA, "eviction launch: %s", cudaGetErrorString(e));
+  return ok_status();
+}
+
+fmha_status fmha_cache_compact(const fmha_cache_args* a, const fmha_cache_args* out, const int32_t* keep,
+                               int64_t keep_stride_b, int64_t keep_stride_h, int32_t n_keep, const int32_t* counts,
+                               const int32_t* dst_start, const float* weights, int32_t n_weights, float* weights_out,
+                               int32_t n_weights_out, cudaStream_t stream) {
+  if (a == nullptr) return fail(FMHA_ERR_INVALID_ARG, "args is NULL");
+  if (!sizes_ok(a) || n_keep < 0 || n_weights < 0 || n_weights_out < 0 || keep_stride_b < 0 || keep_stride_h < 0)
+    return fail(FMHA_ERR_INVALID_ARG, "negative size or stride");
+  if (a->B == 0 || a->Hkv == 0) return ok_status();
+  if (out != nullptr && (out->B != a->B || out->Hkv != a->Hkv || out->D != a->D))
+    return fail(FMHA_ERR_INVALID_ARG, "the caches differ in B, Hkv or D");
+  if (n_keep > 0 && (keep == nullptr || (reinterpret_cast<uintptr_t>(keep) & 3u)))
+    return fail(FMHA_ERR_INVALID_ARG, "keep is NULL or misaligned");
+  if (counts == nullptr || ((reinterpret_cast<uintptr_t>(counts) | reinterpret_cast<uintptr_t>(dst_start)) & 3u))
+    return fail(FMHA_ERR_INVALID_ARG, "counts is NULL, or counts or dst_start misaligned");
+  if ((weights == nullptr) != (weights_out == nullptr))
+    return fail(FMHA_ERR_INVALID_ARG, "weights and weights_out go together");
+  if (weights != nullptr && (out == nullptr) != (weights == weights_out))
+    return fail(FMHA_ERR_INVALID_ARG, "weights_out is weights exactly when the rows move inside one cache");
+  if (weights != nullptr && out == nullptr && n_weights != n_weights_out)
+    return fail(FMHA_ERR_INVALID_ARG, "n_weights and n_weights_out differ");
+  if ((reinterpret_cast<uintptr_t>(weights) | reinterpret_cast<uintptr_t>(weights_out)) & 3u)
+    return fail(FMHA_ERR_INVALID_ARG, "weights misaligned");
+  if (n_keep > INT32_MAX / 2 || n_weights_out > INT32_MAX / 2)
+    return fail(FMHA_ERR_UNSUPPORTED, "more than 2^30 tokens per sequence");
+  // The caches' own checks want lens; these calls have none.
+  CompactParams p;
+  memset(&p, 0, sizeof(p));
+  CacheView co;
+  bool k8, v8, ok8, ov8;
+  fmha_status st;
+  fmha_cache_args x = *a;
+  memset(&x.sf_k, 0, sizeof(x.sf_k));
+  memset(&x.sf_v, 0, sizeof(x.sf_v));
+  x.lens = counts;
+  x.q_lens = nullptr;
+  x.lse = nullptr;
+  if ((st = check_cache(&x, false, true, &p.c, &k8, &v8)) != FMHA_OK) return st;
+  const fmha_cache_args* o = a;
+  co = p.c;
+  if (out != nullptr) {
+    o = out;
+    fmha_cache_args y = *out;
+    memset(&y.sf_k, 0, sizeof(y.sf_k));
+    memset(&y.sf_v, 0, sizeof(y.sf_v));
+    y.lens = counts;
+    y.q_lens = nullptr;
+    y.lse = nullptr;
+    if ((st = check_cache(&y, false, true, &co, &ok8, &ov8)) != FMHA_OK) return st;
+    if (ok8 != k8 || ov8 != v8) return fail(FMHA_ERR_INVALID_ARG, "the caches differ in dtype");
+  }
+  if (static_cast<int64_t>(a->B) * a->Hkv > (out == nullptr ? INT32_MAX : 65535))
+    return fail(FMHA_ERR_UNSUPPORTED, "grid too large");
+  const int ek = k8 ? 1 : 2, ev = v8 ? 1 : 2;
+  p.k = static_cast<const uint8_t*>(a->k.ptr); p.v = static_cast<const uint8_t*>(a->v.ptr);
+  p.k_sb = a->k.stride_b * ek; p.k_ss = a->k.stride_s * ek; p.k_sh = a->k.stride_h * ek;
+  p.v_sb = a->v.stride_b * ev; p.v_ss = a->v.stride_s * ev; p.v_sh = a->v.stride_h * ev;
+  p.k_out = static_cast<uint8_t*>(o->k.ptr); p.v_out = static_cast<uint8_t*>(o->v.ptr);
+  p.ko_sb = o->k.stride_b * ek; p.ko_ss = o->k.stride_s * ek; p.ko_sh = o->k.stride_h * ek;
+  p.vo_sb = o->v.stride_b * ev; p.vo_ss = o->v.stride_s * ev; p.vo_sh = o->v.stride_h * ev;
+  p.out_table = co.page_table; p.out_pages = co.num_pages; p.out_page_shift = co.page_shift;
+  p.out_max_pages = co.max_pages; p.out_capacity = co.capacity;
+  p.keep = keep; p.keep_sb = keep_stride_b; p.keep_sh = keep_stride_h; p.n_keep = n_keep;
+  p.counts = counts;
+  p.dst_start = dst_start;
+  p.weights = weights; p.weights_out = weights_out;
+  p.n_weights = n_weights; p.n_weights_out = n_weights_out;
+  p.k_bytes = a->D * ek;
+  p.v_bytes = a->D * ev;
+  p.in_place = out == nullptr ? 1 : 0;
+  cudaError_t e = launch_compact(p, stream);
+  if (e != cudaSuccess) return fail(FMHA_ERR_CUDA, "compaction launch: %s", cudaGetErrorString(e));
   return ok_status();
 }
 

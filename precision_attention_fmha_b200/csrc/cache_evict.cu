@@ -1,0 +1,308 @@
+// cache_evict.cu -- which keys stay in a cache under a budget, and the cache
+// with the kept rows moved together.
+//
+// Kept of n > budget keys: the first `sinks`, the last `recent`, and of the
+// others the heaviest, ties to the lowest position: the set does not depend on
+// how the work is spread. n <= budget keeps everything.
+#include <algorithm>
+
+#include "cache_tiles.cuh"
+
+namespace fmha {
+namespace {
+
+// Orders like the floats (a larger weight has a larger key; -0 counts as +0, a NaN weighs less than anything).
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  if (!(w == w)) return 0u;
+  const uint32_t v = __float_as_uint(w + 0.f);
+  return (v & 0x80000000u) ? ~v : v | 0x80000000u;
+}
+
+constexpr int kEvictThreads = 1024, kEvictWarps = kEvictThreads / 32;
+
+// One CTA per (sequence, KV head): the `left`-th largest weight digit by digit
+// (11 + 11 + 10 bits), then the kept positions in ascending order.
+__global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
+  __shared__ unsigned hist[2048];
+  __shared__ unsigned sums[kEvictWarps];
+  __shared__ unsigned found[3];  // digit, rank inside it, its size
+  __shared__ int warp_gt[kEvictWarps], warp_eq[kEvictWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.x / p.c.Hkv, h = blockIdx.x - b * p.c.Hkv;
+  int n = __ldg(p.c.lens + b);
+  const int room = min(p.c.capacity, p.n_weights);
+  if (n < 0 || n > room) {
+    if (tid == 0) atomicOr(p.c.err, kErrLength);
+    n = min(max(n, 0), room);
+  }
+  const float* w = p.weights + (static_cast<int64_t>(b) * p.c.Hkv + h) * p.n_weights;
+  int32_t* keep = p.keep + (static_cast<int64_t>(b) * p.c.Hkv + h) * p.budget;
+  const int count = min(n, p.budget);
+  if (tid == 0 && h == 0) p.counts[b] = count;
+  for (int i = count + tid; i < p.budget; i += kEvictThreads) keep[i] = -1;
+  if (n <= p.budget) {
+    for (int i = tid; i < n; i += kEvictThreads) keep[i] = i;
+    return;
+  }
+  const int m0 = p.sinks, m1 = n - p.recent;  // the others: m0 < m1, since sinks + recent <= budget < n
+  int left = p.budget - p.sinks - p.recent;
+  uint32_t limit = 0xffffffffu;  // keys above it stay, and `left` of those equal to it
+  if (left > 0) {
+    uint32_t prefix = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+      for (int i = tid; i < 2048; i += kEvictThreads) hist[i] = 0u;
+      __syncthreads();
+      for (int i = m0 + tid; i < m1; i += kEvictThreads) {
+        const uint32_t k = weight_key(w[i]);
+        if (pass == 0 || (k >> (shift + bits)) == (prefix >> (shift + bits))) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
+      }
+      __syncthreads();
+      // Thread t holds the two digits 2047 - 2 t and 2046 - 2 t: a scan from the top.
+      const unsigned c0 = hist[2047 - 2 * tid], c1 = hist[2046 - 2 * tid];
+      unsigned run = c0 + c1;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned v = __shfl_up_sync(kFull, run, o);
+        if (lane >= o) run += v;
+      }
+      if (lane == 31) sums[warp] = run;
+      __syncthreads();
+      unsigned before = run - c0 - c1;
+      for (int i = 0; i < warp; ++i) before += sums[i];
+      const unsigned want = static_cast<unsigned>(left);
+      if (before < want && before + c0 >= want) found[0] = 2047 - 2 * tid, found[1] = want - before, found[2] = c0;
+      before += c0;
+      if (before < want && before + c1 >= want) found[0] = 2046 - 2 * tid, found[1] = want - before, found[2] = c1;
+      __syncthreads();
+      prefix |= found[0] << shift;
+      left = static_cast<int>(found[1]);
+      __syncthreads();
+    }
+    limit = prefix;
+  }
+  // Warps take consecutive runs of positions.
+  const int run = ((n + kEvictWarps - 1) / kEvictWarps + 31) & ~31;
+  const int j0 = min(n, warp * run), j1 = min(n, j0 + run);
+  auto flags = [&](int j, bool& gt, bool& eq) {
+    gt = eq = false;
+    if (j >= j1) return;
+    if (j < m0 || j >= m1) gt = true;
+    else {
+      const uint32_t k = weight_key(w[j]);
+      gt = k > limit;
+      eq = k == limit && left > 0;
+    }
+  };
+  int gt0 = 0, eq0 = 0;
+  for (int j = j0; j < j1; j += 32) {
+    bool g, e;
+    flags(j + lane, g, e);
+    gt0 += __popc(__ballot_sync(kFull, g));
+    eq0 += __popc(__ballot_sync(kFull, e));
+  }
+  if (lane == 0) warp_gt[warp] = gt0, warp_eq[warp] = eq0;
+  __syncthreads();
+  gt0 = eq0 = 0;
+  for (int i = 0; i < warp; ++i) gt0 += warp_gt[i], eq0 += warp_eq[i];
+  const uint32_t below = (1u << lane) - 1u;
+  for (int j = j0; j < j1; j += 32) {
+    bool g, e;
+    flags(j + lane, g, e);
+    const uint32_t bg = __ballot_sync(kFull, g), be = __ballot_sync(kFull, e);
+    const int eqr = eq0 + __popc(be & below);
+    if (g || (e && eqr < left)) keep[gt0 + __popc(bg & below) + min(eqr, left)] = j + lane;
+    gt0 += __popc(bg);
+    eq0 += __popc(be);
+  }
+}
+
+// ------------------------------------------------------------------ compact --
+struct Place {
+  int64_t outer, row;
+  bool ok;
+};
+__device__ __forceinline__ Place place(const int32_t* table, int max_pages, int pages, int shift, int capacity, int b,
+                                       int pos, uint32_t* err) {
+  if (pos < 0 || pos >= capacity) {
+    atomicOr(err, kErrPageIndex);
+    return {0, 0, false};
+  }
+  if (table == nullptr) return {b, pos, true};
+  const int pg = __ldg(table + static_cast<int64_t>(b) * max_pages + (pos >> shift));
+  if (pg < 0 || pg >= pages) {
+    atomicOr(err, kErrPageIndex);
+    return {0, 0, false};
+  }
+  return {pg, pos & ((1 << shift) - 1), true};
+}
+
+// Kept row i of (b, h): where it comes from and where it goes.
+__device__ __forceinline__ bool kept_row(const CompactParams& p, int b, int h, int i, int start, Place& src, Place& dst,
+                                         int& from) {
+  const int32_t* keep = p.keep + b * p.keep_sb + h * p.keep_sh;
+  from = __ldg(keep + i);
+  if (p.in_place && (from < start + i || (i > 0 && __ldg(keep + i - 1) >= from))) {
+    atomicOr(p.c.err, kErrPageIndex);  // moving up or out of order: other rows would be overwritten first
+    return false;
+  }
+  src = place(p.c.page_table, p.c.max_pages, p.c.num_pages, p.c.page_shift, p.c.capacity, b, from, p.c.err);
+  dst = place(p.out_table, p.out_max_pages, p.out_pages, p.out_page_shift, p.out_capacity, b, start + i, p.c.err);
+  return src.ok && dst.ok;
+}
+
+__device__ __forceinline__ int kept_count(const CompactParams& p, int b) {
+  int n = __ldg(p.counts + b);
+  if (n < 0 || n > p.n_keep) {
+    atomicOr(p.c.err, kErrLength);
+    n = min(max(n, 0), p.n_keep);
+  }
+  return n;
+}
+
+// Into another cache: every row on its own. A warp takes 32 rows, K then V,
+// with eight 16-byte loads per lane in flight.
+constexpr int kCopyRows = 32;
+__global__ void __launch_bounds__(256) compact_copy_kernel(const __grid_constant__ CompactParams p) {
+  const int lane = threadIdx.x & 31;
+  long long item = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int h = static_cast<int>(item % p.c.Hkv);
+  item /= p.c.Hkv;
+  const int runs = (p.n_keep + kCopyRows - 1) / kCopyRows;
+  const int run = static_cast<int>(item % runs);
+  const int b = static_cast<int>(item / runs);
+  if (b >= p.c.B) return;
+  const int count = kept_count(p, b);
+  const int start = p.dst_start != nullptr ? __ldg(p.dst_start + b) : 0;
+  const int i = run * kCopyRows + lane;
+  Place src{0, 0, false}, dst{0, 0, false};
+  int from = 0;
+  bool ok = false;
+  if (i < count) ok = kept_row(p, b, h, i, start, src, dst, from);
+  const int64_t ks = src.outer * p.k_sb + src.row * p.k_ss + h * p.k_sh, vs = src.outer * p.v_sb + src.row * p.v_ss + h * p.v_sh;
+  const int64_t kd = dst.outer * p.ko_sb + dst.row * p.ko_ss + h * p.ko_sh, vd = dst.outer * p.vo_sb + dst.row * p.vo_ss + h * p.vo_sh;
+  if (p.weights_out != nullptr && ok && start + i < p.n_weights_out) {
+    const int64_t bh = static_cast<int64_t>(b) * p.c.Hkv + h;
+    p.weights_out[bh * p.n_weights_out + start + i] = from < p.n_weights ? p.weights[bh * p.n_weights + from] : 0.f;
+  }
+  const uint32_t live = __ballot_sync(kFull, ok);
+  if (live == 0) return;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int lpr = (t ? p.v_bytes : p.k_bytes) / 16, rpl = 32 / lpr;  // lanes per row; rows per load
+    const int sub = lane / lpr, unit = (lane % lpr) * 16;
+    const uint8_t* from_t = (t ? p.v : p.k) + unit;
+    uint8_t* to_t = (t ? p.v_out : p.k_out) + unit;
+    for (int r0 = 0; r0 < kCopyRows; r0 += 8 * rpl) {
+      uint4 x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int r = r0 + k * rpl + sub;
+        const int64_t at = __shfl_sync(kFull, t ? vs : ks, r & 31);
+        if (r < kCopyRows && ((live >> r) & 1u)) x[k] = __ldg(reinterpret_cast<const uint4*>(from_t + at));
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int r = r0 + k * rpl + sub;
+        const int64_t at = __shfl_sync(kFull, t ? vd : kd, r & 31);
+        if (r < kCopyRows && ((live >> r) & 1u)) *reinterpret_cast<uint4*>(to_t + at) = x[k];
+      }
+    }
+  }
+}
+
+// Weights past the kept rows become 0.
+__global__ void __launch_bounds__(256) clear_weights_kernel(const __grid_constant__ CompactParams p) {
+  const int bh = blockIdx.y, b = bh / p.c.Hkv;
+  const int start = (p.dst_start != nullptr ? __ldg(p.dst_start + b) : 0) + kept_count(p, b);
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= max(start, 0) && i < p.n_weights_out) p.weights_out[static_cast<int64_t>(bh) * p.n_weights_out + i] = 0.f;
+}
+
+// Inside one cache: positions never grow (from >= start + i), so rows moved in
+// ascending order never overwrite one that is still to be read. A CTA owns a
+// 32-byte column of the rows of one (sequence, KV head) of K, or V, or the
+// weights, and takes them 512 at a time: all loads, a barrier, all stores.
+constexpr int kMoveThreads = 256, kMoveUnits = 4;
+__global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const __grid_constant__ CompactParams p) {
+  const int cols = p.k_bytes / 32, cols_v = p.v_bytes / 32;  // 32-byte columns of a row
+  const int bh = blockIdx.x, b = bh / p.c.Hkv, h = bh - b * p.c.Hkv;
+  const int what = blockIdx.y;  // columns of K, then of V, then the weights
+  const int count = kept_count(p, b);
+  const int start = p.dst_start != nullptr ? __ldg(p.dst_start + b) : 0;
+  const int tid = threadIdx.x;
+  if (what == cols + cols_v) {
+    float* w = p.weights_out + static_cast<int64_t>(bh) * p.n_weights_out;
+    const int32_t* keep = p.keep + b * p.keep_sb + h * p.keep_sh;
+    for (int r0 = 0; r0 < count; r0 += kMoveThreads * kMoveUnits) {
+      float x[kMoveUnits];
+      int to[kMoveUnits];
+#pragma unroll
+      for (int u = 0; u < kMoveUnits; ++u) {
+        const int i = r0 + u * kMoveThreads + tid;
+        to[u] = -1;
+        if (i >= count) continue;
+        const int from = __ldg(keep + i);
+        if (from < start + i || start + i < 0 || (i > 0 && __ldg(keep + i - 1) >= from)) continue;  // reported with the rows
+        if (start + i >= p.n_weights_out) continue;
+        to[u] = start + i;
+        x[u] = from < p.n_weights_out ? w[from] : 0.f;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < kMoveUnits; ++u)
+        if (to[u] >= 0) w[to[u]] = x[u];
+      __syncthreads();
+    }
+    for (int i = max(0, start + count) + tid; i < p.n_weights_out; i += kMoveThreads) w[i] = 0.f;
+    return;
+  }
+  const bool is_v = what >= cols;
+  const int unit = (what - (is_v ? cols : 0)) * 32 + (tid & 1) * 16;
+  uint8_t* base = (is_v ? p.v_out : p.k_out) + unit;
+  const int64_t sb = is_v ? p.v_sb : p.k_sb, ss = is_v ? p.v_ss : p.k_ss, sh = is_v ? p.v_sh : p.k_sh;
+  constexpr int ROWS = kMoveThreads / 2;
+  for (int r0 = 0; r0 < count; r0 += ROWS * kMoveUnits) {
+    uint4 x[kMoveUnits];
+    uint8_t* to[kMoveUnits];
+#pragma unroll
+    for (int u = 0; u < kMoveUnits; ++u) {
+      const int i = r0 + u * ROWS + (tid >> 1);
+      to[u] = nullptr;
+      if (i >= count) continue;
+      Place src, dst;
+      int from;
+      if (!kept_row(p, b, h, i, start, src, dst, from) || from == start + i) continue;
+      x[u] = *reinterpret_cast<const uint4*>(base + src.outer * sb + src.row * ss + h * sh);
+      to[u] = base + dst.outer * sb + dst.row * ss + h * sh;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kMoveUnits; ++u)
+      if (to[u] != nullptr) *reinterpret_cast<uint4*>(to[u]) = x[u];
+    __syncthreads();
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t s) {
+  evict_select_kernel<<<p.c.B * p.c.Hkv, kEvictThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_compact(const CompactParams& p, cudaStream_t s) {
+  if (p.in_place) {
+    compact_move_kernel<<<dim3(p.c.B * p.c.Hkv, p.k_bytes / 32 + p.v_bytes / 32 + (p.weights_out != nullptr ? 1 : 0)), kMoveThreads, 0, s>>>(p);
+    return cudaGetLastError();
+  }
+  const long long items = static_cast<long long>(p.c.B) * p.c.Hkv * ((p.n_keep + kCopyRows - 1) / kCopyRows);
+  if (items > 0) compact_copy_kernel<<<static_cast<unsigned>((items + 7) / 8), 256, 0, s>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || p.weights_out == nullptr || p.n_weights_out == 0) return e;
+  clear_weights_kernel<<<dim3((p.n_weights_out + 255) / 256, p.c.B * p.c.Hkv), 256, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace fmha

@@ -19,8 +19,19 @@ struct CacheView {
   uint64_t wait_cycles;
 };
 
-struct CacheAttnParams {
+// A call's walk over 64-key tiles (cache_tiles.cuh).
+struct CacheParams {
   CacheView c;
+  int32_t piece_shift;        // log2 of the rows of one TMA copy (16, 32 or 64)
+  int32_t row_tiles;          // tiles of query rows per KV head
+  int32_t n_ctas, min_tiles;  // grid, and the least key tiles a CTA takes
+  // picked blocks: [B, T, Hkv, top], a negative id is no block; key tiles of an item, and how CTAs share them
+  const int32_t* blocks;
+  int32_t top, block_shift, n_blocks;
+  int32_t item_tiles, n_splits, per_split;
+};
+
+struct CacheAttnParams : CacheParams {
   const uint16_t* q; int64_t q_sb, q_ss, q_sh;  // bf16 bits
   uint16_t* o; int64_t o_sb, o_ss, o_sh;
   float* lse;  // nullable [B, Hq, T]
@@ -29,12 +40,6 @@ struct CacheAttnParams {
   const float* sf_v; int32_t sf_v_kind;
   // tree: byte (b, i, j) at mask[b * mask_sb + i * T + j]; nullptr: node i sees nodes 0..i
   const uint8_t* mask; int64_t mask_sb;
-  // picked blocks (nullptr: tree mode): [B, T, Hkv, top], a negative id is no block
-  const int32_t* blocks; int32_t top, block_shift, n_blocks;
-  int32_t piece_shift;  // log2 of the rows of one TMA copy (16, 32 or 64)
-  int32_t row_tiles;    // row tiles of 16 * WM packed rows
-  int32_t n_ctas, min_tiles;  // tree: grid, and the least key tiles a CTA takes
-  int32_t item_tiles, n_splits, per_split;  // picked: key tiles of an item, and how CTAs share them
   float* part_o;    // [2 * n_ctas][rows per tile][D]
   float* part_lse;  // [2 * n_ctas][rows per tile], log2 units
 };
@@ -45,5 +50,66 @@ inline int cache_attn_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 
 cudaError_t launch_cache_attn(int D, bool k8, bool v8, const CacheAttnParams& p, const CUtensorMap& tk,
                               const CUtensorMap& tv, cudaStream_t stream);
 cudaError_t launch_cache_merge(int D, const CacheAttnParams& p, cudaStream_t stream);
+
+// Attention weight that each cached key gathers over the query tokens.
+struct KeyWeightsParams : CacheParams {
+  const uint16_t* q; int64_t q_sb, q_ss, q_sh;
+  const uint8_t* k; int64_t k_sb, k_ss, k_sh;  // strides in elements
+  const float* lse;  // [B, Hq, T]
+  float* weights;    // [B, Hkv, n_weights]
+  int32_t n_weights, causal, accumulate;
+  float scale_log2;
+  const float* sf_k; int32_t sf_k_kind;
+};
+// tq: TMA map of q (boxes of 128 tokens of one head); tk: of k (64-key ring tiles).
+cudaError_t launch_key_weights_few(int D, bool k8, const KeyWeightsParams& p, const CUtensorMap& tk, cudaStream_t s);
+cudaError_t launch_key_weights_many(int D, bool k8, const KeyWeightsParams& p, const CUtensorMap& tq, cudaStream_t s);
+
+// Keys that stay in a cache under a budget.
+struct EvictParams {
+  CacheView c;
+  const float* weights; int32_t n_weights;
+  int32_t budget, sinks, recent;
+  int32_t* keep;    // [B, Hkv, budget]
+  int32_t* counts;  // [B]
+};
+cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t s);
+
+// Moves the kept rows of a cache together.
+struct CompactParams {
+  CacheView c;
+  const uint8_t *k, *v; int64_t k_sb, k_ss, k_sh, v_sb, v_ss, v_sh;      // strides in bytes
+  uint8_t *k_out, *v_out; int64_t ko_sb, ko_ss, ko_sh, vo_sb, vo_ss, vo_sh;
+  const int32_t* out_table; int32_t out_pages, out_page_shift, out_max_pages, out_capacity;
+  const int32_t* keep; int64_t keep_sb, keep_sh; int32_t n_keep;
+  const int32_t* counts;
+  const int32_t* dst_start;  // nullable: rows go to positions dst_start[b] + i
+  const float* weights; float* weights_out; int32_t n_weights, n_weights_out;  // nullable
+  int32_t k_bytes, v_bytes, in_place;  // bytes of a row
+};
+cudaError_t launch_compact(const CompactParams& p, cudaStream_t s);
+
+// Per-block bounds of the cached keys.
+struct KeyBoundsParams {
+  CacheView c;
+  const uint8_t* k; int64_t k_sb, k_ss, k_sh;  // strides in elements
+  uint16_t* bounds;       // bf16 [B, Hkv, n_blocks, 2, D]
+  const int32_t* start;   // nullable [B]: blocks that end at or before it keep their bounds
+  int32_t n_blocks, block_shift;
+};
+cudaError_t launch_key_bounds(int D, bool k8, const KeyBoundsParams& p, cudaStream_t stream);
+
+// Blocks picked for each query tile.
+struct SelectParams {
+  CacheView c;
+  const uint16_t* q; int64_t q_sb, q_ss, q_sh;
+  const uint16_t* bounds;
+  int32_t n_blocks, block_shift, top, sinks, recent;
+  int32_t q_tile, n_tiles;  // query tokens that share a pick; tiles of T
+  int32_t cluster;          // CTAs per item
+  int32_t* list;            // [B, T, Hkv, top], or
+  uint8_t* mask;            // [B, Hkv, n_tiles, n_blocks]
+};
+cudaError_t launch_select_blocks(int D, const SelectParams& p, cudaStream_t stream);
 
 }  // namespace fmha

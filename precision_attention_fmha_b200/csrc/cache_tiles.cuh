@@ -3,12 +3,15 @@
 // from pages (or a contiguous cache) into a shared-memory ring.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "cache_internal.h"
 #include "ptx_sm100.cuh"
 #include "waiter.cuh"
 
 namespace fmha {
 
+constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kTileKeys = 64;  // keys of one ring slot
 constexpr int kGroups = kTileKeys / 16;
 
@@ -83,6 +86,297 @@ __device__ __forceinline__ Piece cache_piece(const CacheView& c, int b, int pos,
     e.row = pos & ((1 << c.page_shift) - 1);
   }
   return e;
+}
+
+// A run of key tiles [t0, t1) of one item.
+struct Seg {
+  int b, t, hkv, rt;
+  int t0, t1, nt;
+  int ctx, nodes;  // tree: context length and nodes in use; keys: cached tokens and query tokens in use
+  int limit;       // keys at or past it do not exist (picked: are hidden)
+};
+
+// The list of key tiles, shared evenly: CTA i takes tiles [i per, (i + 1) per).
+struct Share {
+  long long total;
+  int per;
+};
+
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+// What a walk goes over: a tree's context and nodes, the keys of picked blocks
+// (a fixed number of tiles per item), or all keys of a sequence.
+enum WalkMode : int { WALK_TREE = 0, WALK_PICKED = 1, WALK_KEYS = 2 };
+
+template <int MODE>
+__device__ __forceinline__ SeqLens walk_lens(const CacheView& c, int b, bool& bad) {
+  return MODE == WALK_TREE ? tree_lens(c, b, bad) : seq_lens(c, b, bad);
+}
+template <int MODE>
+__device__ __forceinline__ int tiles_of(const SeqLens s) {
+  return (s.len + (MODE == WALK_TREE ? s.q : 0) + kTileKeys - 1) / kTileKeys;
+}
+
+// Whole warp. Tiles of sequences [0, n), per (KV head, row tile).
+template <int MODE>
+__device__ long long list_tiles(const CacheParams& p, int n, bool report) {
+  long long sum = 0;
+  for (int b = threadIdx.x & 31; b < n; b += 32) {
+    bool bad;
+    sum += tiles_of<MODE>(walk_lens<MODE>(p.c, b, bad));
+    if (bad && report) atomicOr(p.c.err, kErrLength);
+  }
+  return warp_sum(sum);
+}
+template <int MODE>
+__device__ Share list_share(const CacheParams& p, bool report) {
+  Share s;
+  s.total = list_tiles<MODE>(p, p.c.B, report) * p.c.Hkv * p.row_tiles;
+  s.per = static_cast<int>((s.total + p.n_ctas - 1) / p.n_ctas);
+  s.per = max(s.per, p.min_tiles);
+  return s;
+}
+
+// Walks a CTA's segments; every warp keeps its own copy.
+template <int MODE>
+struct Walk {
+  long long pos, end;    // tiles of the list; picked: items
+  int b;                 // current sequence, its first tile in the list and its tiles per item
+  long long base;
+  int nt;
+  SeqLens len;
+
+  __device__ void start(const CacheParams& p) {
+    if constexpr (MODE == WALK_PICKED) {
+      pos = blockIdx.x;
+      end = static_cast<long long>(p.c.B) * p.c.T * p.c.Hkv * p.row_tiles * p.n_splits;
+    } else {
+      const Share s = list_share<MODE>(p, blockIdx.x == 0);
+      pos = min(s.total, static_cast<long long>(blockIdx.x) * s.per);
+      end = min(s.total, pos + s.per);
+      b = -1;
+      base = 0;
+      nt = 0;
+    }
+  }
+
+  __device__ bool next(const CacheParams& p, Seg& g) {
+    if (pos >= end) return false;
+    if constexpr (MODE == WALK_PICKED) {
+      long long item = pos / p.n_splits;
+      const int j = static_cast<int>(pos - item * p.n_splits);
+      pos += gridDim.x;
+      g.rt = static_cast<int>(item % p.row_tiles);
+      item /= p.row_tiles;
+      g.hkv = static_cast<int>(item % p.c.Hkv);
+      item /= p.c.Hkv;
+      g.t = static_cast<int>(item % p.c.T);
+      g.b = static_cast<int>(item / p.c.T);
+      g.nt = p.item_tiles;
+      g.t0 = min(g.nt, j * p.per_split);
+      g.t1 = min(g.nt, g.t0 + p.per_split);
+      bool bad;
+      const SeqLens s = seq_lens(p.c, g.b, bad);
+      if (bad && g.t == 0 && g.hkv == 0) atomicOr(p.c.err, kErrLength);
+      g.limit = g.t < s.q ? s.len - s.q + g.t + 1 : 0;
+      g.ctx = 0x7fffffff;
+      g.nodes = 0;
+    } else {
+      const int lane = threadIdx.x & 31;
+      const int items = p.c.Hkv * p.row_tiles;  // per sequence
+      while (b < 0 || pos >= base + static_cast<long long>(nt) * items) {
+        // 32 sequences at a time: the first whose tiles reach past pos
+        if (b >= 0) base += static_cast<long long>(nt) * items;
+        const int first = b + 1;
+        bool bad;
+        const int bb = first + lane;
+        const SeqLens s = bb < p.c.B ? walk_lens<MODE>(p.c, bb, bad) : SeqLens{0, 0};
+        const int n = tiles_of<MODE>(s);
+        int run = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(kFull, run, o);
+          if (lane >= o) run += v;
+        }
+        const uint32_t past = __ballot_sync(kFull, base + static_cast<long long>(run) * items > pos);
+        const int k = past ? __ffs(past) - 1 : 31;
+        base += static_cast<long long>(__shfl_sync(kFull, run - n, k)) * items;
+        nt = __shfl_sync(kFull, n, k);
+        len.len = __shfl_sync(kFull, s.len, k);
+        len.q = __shfl_sync(kFull, s.q, k);
+        b = first + k;
+        if (b >= p.c.B) return false;  // not reached: pos < total
+      }
+      const long long x = pos - base;
+      const int item = static_cast<int>(x / nt);
+      g.b = b;
+      g.t = 0;
+      g.rt = item % p.row_tiles;
+      g.hkv = item / p.row_tiles;
+      g.nt = nt;
+      g.t0 = static_cast<int>(x - static_cast<long long>(item) * nt);
+      g.t1 = static_cast<int>(min(static_cast<long long>(nt), g.t0 + (end - pos)));
+      g.ctx = len.len;
+      g.nodes = len.q;
+      g.limit = MODE == WALK_TREE ? len.len + len.q : len.len;
+      pos += g.t1 - g.t0;
+    }
+    return true;
+  }
+};
+
+// ---------------------------------------------------------------- producer --
+// Barriers and per-slot metadata of a ring.
+template <int STAGES>
+struct alignas(16) RingMisc {
+  uint64_t full[STAGES], empty[STAGES];
+  TileMeta meta[STAGES];
+  volatile uint32_t abort;
+};
+
+// The producer warp: the tiles of the CTA's walk, in order, into the ring
+// (C::HAS_V: K, then V, of a tile in one slot; else K alone).
+template <class C>
+__device__ void produce(const CacheParams& p, uint8_t* ring, RingMisc<C::STAGES>* misc, const CUtensorMap* tk,
+                        const CUtensorMap* tv, const Waiter w) {
+  using namespace ptx;
+  const int lane = threadIdx.x & 31;
+  const int ps = p.piece_shift, ppt = kTileKeys >> ps;  // pieces per tile
+  constexpr int COPIES = C::KL::CHUNKS + (C::HAS_V ? C::VL::CHUNKS : 0);
+  const int my_piece = lane / COPIES, my_copy = lane - my_piece * COPIES;
+  uint32_t it = 0;
+  bool ok = true;
+  Walk<C::MODE> walk;
+  walk.start(p);
+  Seg g;
+  while (ok && walk.next(p, g)) {
+    // Lane l holds piece `first + l` of the item; the next 32 are fetched early.
+    auto fetch = [&](int i) {
+      Piece e{0, 0, 0, 0};
+      if (i >= g.t1 * ppt) return e;
+      if constexpr (C::MODE == WALK_PICKED) {
+        const int k = p.block_shift - ps;  // pieces per block, log2
+        const int slot = i >> k;
+        if (slot >= p.top) return e;
+        const int id = __ldg(p.blocks + ((static_cast<int64_t>(g.b) * p.c.T + g.t) * p.c.Hkv + g.hkv) * p.top + slot);
+        if (id >= p.n_blocks) atomicOr(p.c.err, kErrPageIndex);
+        if (id < 0 || id >= p.n_blocks) return e;
+        return cache_piece(p.c, g.b, (id << p.block_shift) + ((i & ((1 << k) - 1)) << ps), g.limit);
+      } else {
+        return cache_piece(p.c, g.b, i << ps, g.limit);
+      }
+    };
+    int first = g.t0 * ppt;
+    Piece cur = fetch(first + lane), nxt = fetch(first + 32 + lane);
+    for (int u = g.t0; u < g.t1; ++u) {
+      if (u * ppt - first >= 32) {
+        first += 32;
+        cur = nxt;
+        nxt = fetch(first + 32 + lane);
+      }
+      const int at = u * ppt - first;  // lane of this tile's first piece
+      const int s = it % C::STAGES;
+      const uint32_t ph = (it / C::STAGES) & 1;
+      if (!(ok = __all_sync(kFull, w.wait(smem_addr(&misc->empty[s]), ph ^ 1)))) break;
+      ++it;
+      {  // lanes 0..3: the tile's 16-key groups
+        const int sub = (lane & 3) << 4;
+        const int src = at + (sub >> ps);
+        const int pos = __shfl_sync(kFull, cur.pos, src) + (sub & ((1 << ps) - 1));
+        const int valid = __shfl_sync(kFull, cur.valid, src) - (sub & ((1 << ps) - 1));
+        if (lane < kGroups) {
+          misc->meta[s].pos[lane] = pos;
+          misc->meta[s].valid[lane] = min(16, max(0, valid));
+        }
+      }
+      const int src = (at + my_piece) & 31;
+      const int row = __shfl_sync(kFull, cur.row, src), outer = __shfl_sync(kFull, cur.outer, src);
+      const bool live = __shfl_sync(kFull, cur.valid, src) > 0 && my_piece < ppt;
+      const uint32_t n = __popc(__ballot_sync(kFull, live && my_copy == 0));
+      const uint32_t full = smem_addr(&misc->full[s]);
+      if (lane == 0) mbar_arrive_expect_tx(full, (n << ps) * (C::KL::ROW + (C::HAS_V ? C::VL::ROW : 0)));
+      __syncwarp();
+      if (live) {
+        const uint32_t base = smem_addr(ring + s * C::SLOT);
+        if (my_copy < C::KL::CHUNKS)
+          tma_load_4d(base + my_copy * C::KL::CHUNK_BYTES + (my_piece << ps) * C::KL::SPAN, tk, full,
+                      my_copy * C::KL::CHUNK_ELEMS, g.hkv, row, outer);
+        else
+          tma_load_4d(base + C::KL::BYTES + (my_copy - C::KL::CHUNKS) * C::VL::CHUNK_BYTES +
+                          (my_piece << ps) * C::VL::SPAN,
+                      tv, full, (my_copy - C::KL::CHUNKS) * C::VL::CHUNK_ELEMS, g.hkv, row, outer);
+      }
+    }
+  }
+  // Every copy has landed before shared memory goes away.
+  if (lane == 0)
+    for (uint32_t k = it > C::STAGES ? it - C::STAGES : 0; k < it; ++k)
+      w.drain(smem_addr(&misc->full[k % C::STAGES]), (k / C::STAGES) & 1u);
+  __syncwarp();
+}
+
+// ------------------------------------------------------------ conversions --
+// One half of a 16-bit pair (F16 or BF16) in 32 bits.
+template <bool F16>
+__device__ __forceinline__ float half_of(uint32_t x, int hi) {
+  const uint32_t h = hi ? x >> 16 : x & 0xffffu;
+  if constexpr (F16) return __half2float(__ushort_as_half(static_cast<unsigned short>(h)));
+  return __uint_as_float(h << 16);
+}
+// Two E4M3 codes as a BF16 pair (exact: 4 significant bits, exponents -9..8).
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t v) {
+  const uint32_t h = ptx::e4m3x2_to_f16x2(v);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return ptx::pack_bf16x2(f.x, f.y);
+}
+
+// Row h (0: gq, 1: gq + 8) of the 16 x D query fragment of a warp, from D
+// BF16 values at src (live false: zeros), and the factor that its scores take.
+// For E4M3 keys the contraction runs in F16, which holds the codes exactly: the
+// row is brought to [1, 2) by a power of two, so it is exact too, but for
+// values 2^-14 of the row's largest and smaller, which keep an absolute error
+// of 2^-25 of it; and the columns of a fragment are those whose codes one
+// 32-bit word of K holds (4 j .. 4 j + 3 of each 16).
+template <bool K8, int KS>
+__device__ __forceinline__ void load_q(uint32_t (&qf)[KS][4], int h, float& factor, const uint16_t* src, bool live,
+                                       int j) {
+  if constexpr (K8) {
+    uint32_t raw[KS][2];
+    float top = 0.f;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const uint2 v = live ? __ldg(reinterpret_cast<const uint2*>(src + 16 * s + 4 * j)) : make_uint2(0u, 0u);
+      raw[s][0] = v.x;
+      raw[s][1] = v.y;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        top = fmaxf(top, fabsf(half_of<false>(raw[s][e], 0)));
+        top = fmaxf(top, fabsf(half_of<false>(raw[s][e], 1)));
+      }
+    }
+    top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+    int ex = static_cast<int>((__float_as_uint(top) >> 23) & 0xffu);
+    ex = (ex == 0 || ex == 255) ? 127 : min(ex, 253);  // zero rows and infinities as they are
+    const float down = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
+    factor = __uint_as_float(static_cast<uint32_t>(ex) << 23);
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        qf[s][h + 2 * e] = ptx::pack_f16x2(half_of<false>(raw[s][e], 0) * down, half_of<false>(raw[s][e], 1) * down);
+  } else {
+    factor = 1.f;
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        qf[s][h + 2 * e] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * s + 8 * e + 2 * j)) : 0u;
+  }
 }
 
 }  // namespace fmha

@@ -92,6 +92,11 @@ def load_library(path=None):
     lib.fmha_fwd_tree_workspace_bytes.argtypes = [cache]
     lib.fmha_fwd_selected.argtypes = [cache, vp, i32, i32, vp, sz, vp]
     lib.fmha_fwd_selected_workspace_bytes.argtypes = [cache, i32, i32]
+    lib.fmha_key_bounds.argtypes = [cache, vp, i32, i32, vp, vp]
+    lib.fmha_select_blocks.argtypes = [cache, vp, i32, i32, i32, i32, i32, i32, vp, vp]
+    lib.fmha_key_weights.argtypes = [cache, vp, i32, i32, i32, vp]
+    lib.fmha_evict_select.argtypes = [cache, vp, i32, i32, i32, i32, vp, vp, vp]
+    lib.fmha_cache_compact.argtypes = [cache, cache, vp, i64, i64, i32, vp, vp, vp, i32, vp, i32, vp]
     for f in ("fmha_fwd_tree_workspace_bytes", "fmha_fwd_selected_workspace_bytes"):
         getattr(lib, f).restype = sz
     lib.fmha_status_string.argtypes = [ctypes.c_int]
@@ -546,3 +551,144 @@ def fmha_fwd_selected(q, k, v, blocks, lens, block, q_lens=None, page_table=None
         workspace, ptr, size = _scratch(workspace, need, q.device)
         _check(lib.fmha_fwd_selected(ctypes.byref(a), ids, top, int(block), ptr, size, s))
     return out
+
+
+def key_bounds(k, lens, block, page_table=None, bounds=None, start=None, stream=None):
+    """Smallest and largest key of each `block`-key block (16, 32, 64 or 128) and channel.
+
+    k: [B, S, Hkv, D], or a page pool with page_table; lens: int32 [B], tokens in the cache. Returns bounds BF16
+    [B, Hkv, n_blocks, 2, D] (minima, maxima); blocks past a sequence's end are left as they were (zeros when
+    allocated here). start: int32 [B]: blocks that end at or before it are left, so that a step refreshes the
+    newest block only."""
+    a = _cache_args(k, lens, page_table)
+    if bounds is None:
+        shape = (a.B, a.Hkv, -(-a.capacity // block) if block > 0 else 0, 2, a.D)
+    else:
+        shape = tuple(bounds.shape)
+        if (bounds.dtype != torch.bfloat16 or len(shape) != 5 or shape[:2] != (a.B, a.Hkv) or shape[3:] != (2, a.D)
+                or not bounds.is_contiguous()):
+            raise ValueError(f"bounds must be contiguous BF16 [{a.B}, {a.Hkv}, n_blocks, 2, {a.D}]")
+    start_ptr = _ints(start, (a.B,), "start")
+    lib = load_library()
+    with _launch(stream, k, lens, page_table, bounds, start) as s:
+        if bounds is None:
+            bounds = torch.zeros(shape, dtype=torch.bfloat16, device=k.device)
+        _check(lib.fmha_key_bounds(ctypes.byref(a), bounds.data_ptr(), shape[2], int(block), start_ptr, s))
+    return bounds
+
+
+def select_blocks(q, bounds, lens, block, top, sink_blocks=0, recent_blocks=1, q_lens=None, q_tile=1, out=None,
+                  stream=None):
+    """Picks the blocks of keys that each query attends to, by the score sum_h sum_d max(q_hd min_jd, q_hd max_jd).
+
+    q: BF16 [B, T, Hq, D], the last q_lens[b] (None: T) of the lens[b] tokens; bounds as from ``key_bounds``. The
+    first sink_blocks and the last recent_blocks in sight are picked first, then the best scores, up to `top`.
+    q_tile 1: int32 [B, T, Hkv, top], ascending ids then -1, for ``fmha_fwd_selected``. q_tile 128 (block 128):
+    the uint8 mask [B, Hkv, ceil(T/128), n_blocks] of ``fmha_fwd_block_sparse`` / ``fmha_fwd_paged``, picked by
+    tiles of 128 query tokens."""
+    if (bounds.dtype != torch.bfloat16 or bounds.dim() != 5 or bounds.shape[3] != 2 or not bounds.is_contiguous()
+            or q.dim() != 4 or bounds.shape[0] != q.shape[0] or bounds.shape[4] != q.shape[3]):
+        raise ValueError("bounds must be contiguous BF16 [B, Hkv, n_blocks, 2, D] for q [B, T, Hq, D]")
+    B, T, Hq, D = q.shape
+    Hkv, n_blocks = bounds.shape[1], bounds.shape[2]
+    a = _CacheArgs()
+    a.q = _tensor(q)
+    a.B, a.T, a.Hq, a.Hkv, a.D = B, T, Hq, Hkv, D
+    a.lens, a.q_lens = _ints(lens, (B,), "lens"), _ints(q_lens, (B,), "q_lens")
+    shape, dtype = ((B, T, Hkv, int(top)), torch.int32) if q_tile == 1 else ((B, Hkv, -(-T // 128), n_blocks), torch.uint8)
+    if out is not None and (out.dtype != dtype or tuple(out.shape) != shape or not out.is_contiguous()):
+        raise ValueError(f"out must be a contiguous {dtype} tensor of shape {list(shape)}")
+    lib = load_library()
+    with _launch(stream, q, bounds, lens, q_lens, out) as s:
+        if out is None:
+            out = torch.empty([max(0, n) for n in shape], dtype=dtype, device=q.device)
+        _check(lib.fmha_select_blocks(ctypes.byref(a), bounds.data_ptr(), n_blocks, int(block), int(top),
+                                      int(sink_blocks), int(recent_blocks), int(q_tile), out.data_ptr(), s))
+    return out
+
+
+def key_weights(q, k, lse, weights, lens, q_lens=None, page_table=None, causal=True, accumulate=True,
+                sf_k=None, softmax_scale=None, stream=None):
+    """Adds (accumulate=False: writes) to weights fp32 [B, Hkv, n] the attention weight each key gathers over q.
+
+    weights[b, h, s] (+)= sum_t sum_g exp(scale * q_tg . k_s - lse[b, g, t]), over the query heads g of KV head h
+    and the tokens t that see key s. lse: contiguous fp32 [B, Hq, T] of the attention call on the same q and keys.
+    q holds the last q_lens[b] (None: T) of the lens[b] tokens. Entries past lens[b] are left as they were."""
+    a = _cache_args(k, lens, page_table, q=q, q_lens=q_lens, sf_k=sf_k, softmax_scale=softmax_scale, lse=lse)
+    if weights.dim() != 3:
+        raise ValueError("weights must be a contiguous float32 [B, Hkv, n] tensor")
+    w = _floats(weights, (a.B, a.Hkv, weights.shape[2]), "weights")
+    lib = load_library()
+    with _launch(stream, q, k, lse, weights, lens, q_lens, page_table, *_sf_tensors(sf_k)) as s:
+        _check(lib.fmha_key_weights(ctypes.byref(a), w, weights.shape[2], 1 if causal else 0, 1 if accumulate else 0, s))
+    return weights
+
+
+def evict_select(weights, lens, budget, sinks=0, recent=0, keep=None, counts=None, stream=None):
+    """The positions that stay in the cache of each (sequence, KV head) under `budget` keys.
+
+    weights: contiguous fp32 [B, Hkv, n]; lens: int32 [B]. Returns (keep int32 [B, Hkv, budget]: ascending positions,
+    then -1; counts int32 [B]: min(lens, budget)). The first `sinks` and last `recent` positions always stay, then
+    the largest weights, ties to the lowest position."""
+    if weights.dim() != 3:
+        raise ValueError("weights must be a contiguous float32 [B, Hkv, n] tensor")
+    B, Hkv, n = weights.shape
+    a = _CacheArgs()
+    a.B, a.Hkv = B, Hkv
+    a.lens = _ints(lens, (B,), "lens")
+    w = _floats(weights, (B, Hkv, n), "weights")
+    _ints(keep, (B, Hkv, budget), "keep")
+    _ints(counts, (B,), "counts")
+    lib = load_library()
+    with _launch(stream, weights, lens, keep, counts) as s:
+        if keep is None:
+            keep = torch.empty((B, Hkv, max(0, budget)), dtype=torch.int32, device=weights.device)
+        if counts is None:
+            counts = torch.empty((B,), dtype=torch.int32, device=weights.device)
+        _check(lib.fmha_evict_select(ctypes.byref(a), w, n, int(budget), int(sinks), int(recent), keep.data_ptr(),
+                                     counts.data_ptr(), s))
+    return keep, counts
+
+
+def cache_compact(k, v, keep, counts, dst_start=None, page_table=None, k_out=None, v_out=None, out_page_table=None,
+                  weights=None, weights_out=None, stream=None):
+    """Moves the kept rows of a cache together: position keep[b, h, i] -> dst_start[b] + i (None: i), i < counts[b].
+
+    keep: int32 [B, Hkv or 1, n] (unit last stride); counts, dst_start: int32 [B]. Without k_out / v_out the rows
+    move inside the cache: positions ascend with i, keep[b, h, i] >= dst_start[b] + i, and no page belongs to two
+    sequences. With them (and out_page_table when paged) they are copied into another cache, in any order.
+    weights fp32 [B, Hkv, n] move along (to weights_out with another cache); entries past the moved ones become 0.
+    Returns (k_out, v_out)."""
+    B = page_table.shape[0] if page_table is not None else k.shape[0]
+    if counts is None:
+        raise ValueError("counts must be a contiguous int32 tensor")
+    a = _cache_args(k, counts, page_table, v=v)
+    if keep.dtype != torch.int32 or keep.dim() != 3 or keep.shape[0] != B or keep.shape[1] not in (1, a.Hkv) or (
+            keep.shape[2] > 1 and keep.stride(2) != 1):
+        raise ValueError(f"keep must be int32 [{B}, {a.Hkv} or 1, n] with unit last stride")
+    start = _ints(dst_start, (B,), "dst_start")
+    if (k_out is None) != (v_out is None) or (k_out is None and (out_page_table is not None or weights_out is not None)):
+        raise ValueError("another cache needs k_out and v_out (and, when paged, out_page_table)")
+    o = None
+    if k_out is not None:
+        if k_out.dtype != k.dtype or v_out.dtype != v.dtype or k_out.shape[2:] != k.shape[2:]:
+            raise ValueError("k_out / v_out must have the dtypes, heads and head dim of k / v")
+        o = _cache_args(k_out, counts, out_page_table, v=v_out)
+        if (weights is None) != (weights_out is None):
+            raise ValueError("weights and weights_out go together")
+    w = wo = None
+    nw = nwo = 0
+    if weights is not None:
+        if weights.dim() != 3 or (weights_out is not None and weights_out.dim() != 3):
+            raise ValueError("weights must be contiguous float32 [B, Hkv, n] tensors")
+        w, nw = _floats(weights, (B, a.Hkv, weights.shape[2]), "weights"), weights.shape[2]
+        wo, nwo = w, nw
+        if weights_out is not None:
+            wo, nwo = _floats(weights_out, (B, a.Hkv, weights_out.shape[2]), "weights_out"), weights_out.shape[2]
+    lib = load_library()
+    with _launch(stream, k, v, keep, counts, dst_start, page_table, k_out, v_out, out_page_table, weights,
+                 weights_out) as s:
+        _check(lib.fmha_cache_compact(ctypes.byref(a), ctypes.byref(o) if o is not None else None, keep.data_ptr(),
+                                      keep.stride(0) if B > 1 else 0, keep.stride(1) if keep.shape[1] > 1 else 0,
+                                      keep.shape[2], counts.data_ptr(), start, w, nw, wo, nwo, s))
+    return (k, v) if k_out is None else (k_out, v_out)

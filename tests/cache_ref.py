@@ -113,3 +113,76 @@ def check(o, lse, ref, v8=False):
         off = (lse.double() - rl).abs()[~dead]
         lim = (LSE_ATOL + rl.abs() * 2.0 ** -18)[~dead]
         assert bool((off <= lim).all()), f"lse off by {float(off.max()):.3g}"
+
+
+def bounds(k, lens, block, before, table=None):
+    """The bounds buffer after the call; `before` is what it held."""
+    out = before.double().clone()
+    for b in range(out.shape[0]):
+        kk = gather(k, table, b, int(lens[b])).double()
+        for j in range(-(-int(lens[b]) // block)):
+            part = kk[j * block: (j + 1) * block]
+            out[b, :, j, 0], out[b, :, j, 1] = part.amin(0), part.amax(0)
+    return out
+
+
+def pick(q, bnd, lens, block, top, sinks, recent, q_lens=None, q_tile=1):
+    """Picked ids of each (sequence, tile, KV head), as nested lists."""
+    B, T, Hq, D = q.shape
+    Hkv = bnd.shape[1]
+    G = Hq // Hkv
+    out = []
+    for b in range(B):
+        m = T if q_lens is None else int(q_lens[b])
+        rows = []
+        for t0 in range(0, T, q_tile):
+            t1 = min(t0 + q_tile, m)
+            last = int(lens[b]) - m + t1 - 1
+            seen = last // block + 1 if t1 > t0 and last >= 0 else 0
+            heads = []
+            for h in range(Hkv):
+                x = q[b, t0:t1, h * G:(h + 1) * G].double().reshape(-1, D)
+                lo, hi = bnd[b, h, :seen, 0].double(), bnd[b, h, :seen, 1].double()
+                score = torch.maximum(x[:, None] * lo, x[:, None] * hi).sum((0, 2)).tolist() if seen else []
+                order = sorted(range(seen), key=lambda j: (not (j < sinks or j >= seen - recent), 0.0 if
+                                                           (j < sinks or j >= seen - recent) else -score[j], j))
+                heads.append(sorted(order[:top]))
+            rows.append(heads)
+        out.append(rows)
+    return out
+
+
+def weights(q, k, lse, lens, n, q_lens=None, table=None, causal=True, sf_k=None, scale=None):
+    """Gathered weights [B, Hkv, n] in 64 bits."""
+    B, T, Hq, D = q.shape
+    Hkv = k.shape[2]
+    G = Hq // Hkv
+    scale = scale or 1 / math.sqrt(D)
+    out = torch.zeros(B, Hkv, n, dtype=torch.float64, device=q.device)
+    for b in range(B):
+        m = T if q_lens is None else int(q_lens[b])
+        s = int(lens[b])
+        kk = gather(k, table, b, s).double()
+        at = s - m + torch.arange(m, device=q.device)
+        sees = (torch.arange(s, device=q.device) <= at[:, None]) if causal else torch.ones(m, s, dtype=torch.bool, device=q.device)
+        for h in range(Hq):
+            z = (q[b, :m, h].double() @ (kk[:, h // G] * scale_of(sf_k, b, h // G)).t()) * scale - lse[b, h, :m].double()[:, None]
+            out[b, h // G, :s] += torch.where(sees, z.exp(), torch.zeros_like(z)).sum(0)
+    return out
+
+
+def kept(w, lens, budget, sinks, recent):
+    """Kept positions of each (sequence, KV head), as nested lists."""
+    out = []
+    for b in range(w.shape[0]):
+        n = int(lens[b])
+        heads = []
+        for h in range(w.shape[1]):
+            if n <= budget:
+                heads.append(list(range(n)))
+                continue
+            x = w[b, h, :n].tolist()
+            rest = sorted(range(sinks, n - recent), key=lambda s: (x[s] != x[s], -x[s] if x[s] == x[s] else 0.0, s))
+            heads.append(sorted(list(range(sinks)) + list(range(n - recent, n)) + rest[: budget - sinks - recent]))
+        out.append(heads)
+    return out
