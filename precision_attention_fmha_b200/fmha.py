@@ -11,10 +11,10 @@ factor is given as ``Scale(tensor, kind, rows_per_block)`` with ``kind`` one
 of "per_tensor", "per_head", "per_token_block", "per_channel".
 """
 
-import contextlib
 import ctypes
 import math
 import os
+import struct
 from collections import namedtuple
 
 import torch
@@ -87,7 +87,7 @@ def load_library(path=None):
     lib.fmha_decode_workspace_bytes.restype = sz
     lib.fmha_decode_num_splits.argtypes = [ctypes.POINTER(_Args), i32]
     lib.fmha_decode_num_splits.restype = i32
-    cache = ctypes.POINTER(_CacheArgs)
+    cache = vp  # packed fmha_cache_args (_CACHE_ARGS), or a pointer to a _CacheArgs
     lib.fmha_fwd_tree.argtypes = [cache, vp, i64, vp, sz, vp]
     lib.fmha_fwd_tree_workspace_bytes.argtypes = [cache]
     lib.fmha_fwd_selected.argtypes = [cache, vp, i32, i32, vp, sz, vp]
@@ -400,92 +400,132 @@ class _CacheArgs(ctypes.Structure):
                 ("softmax_scale", ctypes.c_float), ("lse", ctypes.c_void_p)]
 
 
-@contextlib.contextmanager
-def _launch(stream, *tensors):
+# The same layout as packed values: one call fills the 45 members, where setting them one by one in the structure
+# took 16 us of a decoding step's host time (packed: 5 us).
+_CACHE_ARGS = struct.Struct("@" + 4 * "Pii3q" + 2 * "Pii" + "6i3P3ifP")
+_NO_TENSOR, _NO_SF = (0, 0, 0, 0, 0, 0), (0, 0, 0)
+_DTYPES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float8_e4m3fn: E4M3, torch.int8: INT8}
+
+
+class _launch:
     """Makes the tensors' device current, and `stream` (None: that device's current stream) the stream that
-    outputs and workspaces allocated inside belong to. Yields the stream handle."""
-    devices = {t.device for t in tensors if t is not None}
-    if len(devices) != 1 or next(iter(devices)).type != "cuda":
-        raise ValueError(f"all tensors must be on one CUDA device, got {sorted(map(str, devices))}")
-    device = devices.pop()
-    with torch.cuda.device(device):
-        if stream is None:
-            stream = torch.cuda.current_stream(device)
-        elif stream.device != device:
-            raise ValueError(f"stream of {stream.device} for tensors of {device}")
-        with torch.cuda.stream(stream):
-            yield ctypes.c_void_p(stream.cuda_stream)
+    outputs and workspaces allocated inside belong to. Entering gives the stream handle."""
+
+    __slots__ = ("contexts", "stream", "device")
+
+    def __init__(self, stream, *tensors):
+        devices = {t.get_device() for t in tensors if t is not None}
+        device = devices.pop()
+        if devices or device < 0:
+            raise ValueError("all tensors must be on one CUDA device, got "
+                             f"{sorted({str(t.device) for t in tensors if t is not None})}")
+        if stream is not None and stream.device.index != device:
+            raise ValueError(f"stream of {stream.device} for tensors of cuda:{device}")
+        self.stream, self.device, self.contexts = stream, device, ()
+
+    def __enter__(self):
+        if self.device != torch.cuda.current_device():
+            self.contexts += (torch.cuda.device(self.device),)
+        if self.stream is not None:
+            self.contexts += (torch.cuda.stream(self.stream),)
+        for c in self.contexts:
+            c.__enter__()
+        return (self.stream or torch.cuda.current_stream(self.device)).cuda_stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
+
+
+def _array(t, dtype, shape, what):
+    """Checks a tensor's type, shape and contiguity; returns its address (0 for None)."""
+    if t is None:
+        return 0
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {list(shape)}")
+    return t.data_ptr()
 
 
 def _ints(t, shape, what):
-    """Checks an int32 tensor's shape and contiguity; returns its address (None for None)."""
-    if t is None:
-        return None
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous int32 tensor of shape {list(shape)}")
-    return t.data_ptr()
+    return _array(t, torch.int32, shape, what)
 
 
 def _floats(t, shape, what):
-    if t is None:
-        return None
-    if t.dtype != torch.float32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous float32 tensor of shape {list(shape)}")
-    return t.data_ptr()
+    return _array(t, torch.float32, shape, what)
+
+
+def _packed(t):
+    stride = t.stride()
+    if len(stride) != 4 or stride[3] != 1:
+        raise ValueError("expected a [B, S, H, D] tensor with a contiguous last dim")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return (t.data_ptr(), code, 0, stride[0], stride[1], stride[2])
 
 
 def _cache_sf(s, B, Hkv, what):
-    if s is not None and s.kind == "per_head" and tuple(s.tensor.shape) != (B, Hkv):
+    if s is None:
+        return _NO_SF
+    sf = _sf(s)
+    if s.kind == "per_head" and tuple(s.tensor.shape) != (B, Hkv):
         raise ValueError(f"{what}: per-head scales must have shape [{B}, {Hkv}]")
-    if s is not None and s.tensor.numel() == 0:
+    if s.kind not in (None, "none") and s.tensor.numel() == 0:
         raise ValueError(f"{what}: empty scale tensor")
-    return _sf(s)
+    return (sf.ptr or 0, sf.kind, sf.rows_per_block)
 
 
 def _cache_args(k, lens, page_table, q=None, v=None, out=None, q_lens=None, sf_k=None, sf_v=None,
                 softmax_scale=None, lse=None):
-    """_CacheArgs of k (and v) [B, S, Hkv, D], or pools [pages, page_size, Hkv, D] with a page table [B, max_pages]."""
-    a = _CacheArgs()
-    a.k = _tensor(k)
-    a.Hkv, a.D = k.shape[2], k.shape[3]
+    """fmha_cache_args of k (and v) [B, S, Hkv, D], or pools [pages, page_size, Hkv, D] with a page table
+    [B, max_pages]; and (B, Hkv, D, capacity)."""
+    tk = _packed(k)
+    n, rows, Hkv, D = k.shape
     if page_table is not None:
         if page_table.dim() != 2:
             raise ValueError("page_table must be contiguous int32 [B, max_pages_per_seq]")
-        a.B = page_table.shape[0]
-        a.page_table = _ints(page_table, page_table.shape, "page_table")
-        a.num_pages, a.page_size, a.max_pages_per_seq = k.shape[0], k.shape[1], page_table.shape[1]
-        a.capacity = a.max_pages_per_seq * a.page_size
+        B, per = page_table.shape
+        table = (_ints(page_table, page_table.shape, "page_table"), n, rows, per)
+        capacity = per * rows
     else:
-        a.B, a.capacity = k.shape[0], k.shape[1]
+        B, capacity, table = n, rows, (0, 0, 0, 0)
+    tv = tq = to = _NO_TENSOR
     if v is not None:
         if v.shape != k.shape:
             raise ValueError(f"k {list(k.shape)} and v {list(v.shape)} differ in shape")
-        a.v = _tensor(v)
-    a.lens = _ints(lens, (a.B,), "lens")
-    a.q_lens = _ints(q_lens, (a.B,), "q_lens")
-    a.sf_k, a.sf_v = _cache_sf(sf_k, a.B, a.Hkv, "sf_k"), _cache_sf(sf_v, a.B, a.Hkv, "sf_v")
+        tv = _packed(v)
+    T = Hq = lse_ptr = 0
     if q is not None:
-        a.q = _tensor(q)
-        if q.shape[0] != a.B or q.shape[3] != a.D:
-            raise ValueError(f"q {list(q.shape)} does not fit a cache of {a.B} sequences with head dim {a.D}")
-        a.T, a.Hq = q.shape[1], q.shape[2]
-        a.lse = _floats(lse, (a.B, a.Hq, a.T), "lse")
+        tq = _packed(q)
+        if q.shape[0] != B or q.shape[3] != D:
+            raise ValueError(f"q {list(q.shape)} does not fit a cache of {B} sequences with head dim {D}")
+        T, Hq = q.shape[1], q.shape[2]
+        lse_ptr = _floats(lse, (B, Hq, T), "lse")
     if out is not None:
         if out.shape != q.shape:
             raise ValueError(f"out {list(out.shape)} differs from q {list(q.shape)} in shape")
-        a.o = _tensor(out)
-    a.softmax_scale = float(softmax_scale) if softmax_scale else 0.0
-    return a
+        to = _packed(out)
+    args = _CACHE_ARGS.pack(*tq, *tk, *tv, *to, *_cache_sf(sf_k, B, Hkv, "sf_k"), *_cache_sf(sf_v, B, Hkv, "sf_v"),
+                            B, T, Hq, Hkv, D, capacity, _ints(lens, (B,), "lens"), _ints(q_lens, (B,), "q_lens"),
+                            table[0], table[1], table[2], table[3], float(softmax_scale) if softmax_scale else 0.0,
+                            lse_ptr)
+    return args, (B, Hkv, D, capacity)
 
 
-def _scratch(workspace, need, device):
-    """(address, bytes) of the caller's workspace, or of one allocated here."""
+def _scratch(workspace, need, q):
+    """The caller's workspace, or one allocated here; its address and size."""
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    elif workspace.device != device:
-        raise ValueError(f"workspace on {workspace.device}, tensors on {device}")
-    return (workspace, None, 0) if workspace is None else (
-        workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        if need == 0:
+            return None, 0, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != q.get_device():
+        raise ValueError(f"workspace on {workspace.device}, tensors on {q.device}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _out_for(q, out):
+    """O like q, when the caller gives none: its output must be in the arguments before they are packed."""
+    return torch.empty(q.shape, dtype=torch.bfloat16, device=q.device) if out is None else out
 
 
 def _sf_tensors(*scales):
@@ -502,31 +542,28 @@ def fmha_fwd_tree(q, k, v, ctx_lens, tree_mask=None, tree_lens=None, page_table=
     tree_lens: int32 [B], nodes in use (None: T). tree_mask: uint8 [B or 1, T, T], nonzero where node i (row)
     sees node j; None: a chain (node i sees nodes 0..i), so T = 1 is an ordinary decoding step of a ragged batch.
     lse (optional): contiguous fp32 [B, Hq, T]. Rows that see no key give O = 0, lse = -inf."""
-    a = _cache_args(k, ctx_lens, page_table, q=q, v=v, out=out, q_lens=tree_lens, sf_k=sf_k, sf_v=sf_v,
-                    softmax_scale=softmax_scale, lse=lse)
-    mask_sb = 0
+    T = q.shape[1] if q.dim() == 4 else 0
+    mask, mask_sb = 0, 0
     if tree_mask is not None:
-        T = q.shape[1]
-        if (tree_mask.dtype != torch.uint8 or tree_mask.dim() != 3 or tree_mask.shape[0] not in (1, a.B)
-                or tuple(tree_mask.shape[1:]) != (T, T) or (T > 1 and (tree_mask.stride(2) != 1 or tree_mask.stride(1) != T))):
-            raise ValueError(f"tree_mask must be uint8 [{a.B} or 1, {T}, {T}] with contiguous rows")
-        mask_sb = tree_mask.stride(0) if tree_mask.shape[0] > 1 else 0
+        st = tree_mask.stride()
+        if (tree_mask.dtype != torch.uint8 or len(st) != 3 or tree_mask.shape[0] not in (1, q.shape[0])
+                or tree_mask.shape[1:] != (T, T) or (T > 1 and st[1:] != (T, 1))):
+            raise ValueError(f"tree_mask must be uint8 [{q.shape[0]} or 1, {T}, {T}] with contiguous rows")
+        mask, mask_sb = tree_mask.data_ptr(), st[0] if tree_mask.shape[0] > 1 else 0
     lib = load_library()
     with _launch(stream, q, k, v, ctx_lens, tree_mask, tree_lens, page_table, out, lse, *_sf_tensors(sf_k, sf_v)) as s:
-        if out is None:
-            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-            a.o = _tensor(out)
-        need = lib.fmha_fwd_tree_workspace_bytes(ctypes.byref(a))
-        workspace, ptr, size = _scratch(workspace, need, q.device)
-        _check(lib.fmha_fwd_tree(ctypes.byref(a), tree_mask.data_ptr() if tree_mask is not None else None, mask_sb,
-                                 ptr, size, s))
+        out = _out_for(q, out)
+        a, _ = _cache_args(k, ctx_lens, page_table, q=q, v=v, out=out, q_lens=tree_lens, sf_k=sf_k, sf_v=sf_v,
+                           softmax_scale=softmax_scale, lse=lse)
+        workspace, ptr, size = _scratch(workspace, lib.fmha_fwd_tree_workspace_bytes(a), q)
+        _check(lib.fmha_fwd_tree(a, mask, mask_sb, ptr, size, s))
     return out
 
 
 def tree_workspace_bytes(q, k, page_table=None):
     """Workspace bytes fmha_fwd_tree needs for these shapes (host only)."""
     lens = torch.empty(q.shape[0], dtype=torch.int32)
-    return load_library().fmha_fwd_tree_workspace_bytes(ctypes.byref(_cache_args(k, lens, page_table, q=q)))
+    return load_library().fmha_fwd_tree_workspace_bytes(_cache_args(k, lens, page_table, q=q)[0])
 
 
 def fmha_fwd_selected(q, k, v, blocks, lens, block, q_lens=None, page_table=None, workspace=None, out=None,
@@ -536,20 +573,17 @@ def fmha_fwd_selected(q, k, v, blocks, lens, block, q_lens=None, page_table=None
     blocks: contiguous int32 [B, T, Hkv, top], ids of the `block`-key blocks (16, 32, 64 or 128) that query token
     t reads in KV head h; negative: none (``select_blocks`` makes them). lens: int32 [B], tokens in the cache;
     the q_lens[b] (None: T) query tokens are its last ones, and each sees keys up to its own position."""
-    a = _cache_args(k, lens, page_table, q=q, v=v, out=out, q_lens=q_lens, sf_k=sf_k, sf_v=sf_v,
-                    softmax_scale=softmax_scale, lse=lse)
     if blocks.dim() != 4:
         raise ValueError("blocks must be a contiguous int32 [B, T, Hkv, top] tensor")
-    ids = _ints(blocks, (a.B, a.T, a.Hkv, blocks.shape[3]), "blocks")
     top = blocks.shape[3]
+    ids = _ints(blocks, (q.shape[0], q.shape[1], k.shape[2], top), "blocks")
     lib = load_library()
     with _launch(stream, q, k, v, blocks, lens, q_lens, page_table, out, lse, *_sf_tensors(sf_k, sf_v)) as s:
-        if out is None:
-            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-            a.o = _tensor(out)
-        need = lib.fmha_fwd_selected_workspace_bytes(ctypes.byref(a), top, int(block))
-        workspace, ptr, size = _scratch(workspace, need, q.device)
-        _check(lib.fmha_fwd_selected(ctypes.byref(a), ids, top, int(block), ptr, size, s))
+        out = _out_for(q, out)
+        a, _ = _cache_args(k, lens, page_table, q=q, v=v, out=out, q_lens=q_lens, sf_k=sf_k, sf_v=sf_v,
+                           softmax_scale=softmax_scale, lse=lse)
+        workspace, ptr, size = _scratch(workspace, lib.fmha_fwd_selected_workspace_bytes(a, top, int(block)), q)
+        _check(lib.fmha_fwd_selected(a, ids, top, int(block), ptr, size, s))
     return out
 
 
@@ -560,20 +594,20 @@ def key_bounds(k, lens, block, page_table=None, bounds=None, start=None, stream=
     [B, Hkv, n_blocks, 2, D] (minima, maxima); blocks past a sequence's end are left as they were (zeros when
     allocated here). start: int32 [B]: blocks that end at or before it are left, so that a step refreshes the
     newest block only."""
-    a = _cache_args(k, lens, page_table)
+    a, (B, Hkv, D, capacity) = _cache_args(k, lens, page_table)
     if bounds is None:
-        shape = (a.B, a.Hkv, -(-a.capacity // block) if block > 0 else 0, 2, a.D)
+        shape = (B, Hkv, -(-capacity // block) if block > 0 else 0, 2, D)
     else:
         shape = tuple(bounds.shape)
-        if (bounds.dtype != torch.bfloat16 or len(shape) != 5 or shape[:2] != (a.B, a.Hkv) or shape[3:] != (2, a.D)
+        if (bounds.dtype != torch.bfloat16 or len(shape) != 5 or shape[:2] != (B, Hkv) or shape[3:] != (2, D)
                 or not bounds.is_contiguous()):
-            raise ValueError(f"bounds must be contiguous BF16 [{a.B}, {a.Hkv}, n_blocks, 2, {a.D}]")
-    start_ptr = _ints(start, (a.B,), "start")
+            raise ValueError(f"bounds must be contiguous BF16 [{B}, {Hkv}, n_blocks, 2, {D}]")
+    start_ptr = _ints(start, (B,), "start")
     lib = load_library()
     with _launch(stream, k, lens, page_table, bounds, start) as s:
         if bounds is None:
             bounds = torch.zeros(shape, dtype=torch.bfloat16, device=k.device)
-        _check(lib.fmha_key_bounds(ctypes.byref(a), bounds.data_ptr(), shape[2], int(block), start_ptr, s))
+        _check(lib.fmha_key_bounds(a, bounds.data_ptr(), shape[2], int(block), start_ptr, s))
     return bounds
 
 
@@ -591,18 +625,15 @@ def select_blocks(q, bounds, lens, block, top, sink_blocks=0, recent_blocks=1, q
         raise ValueError("bounds must be contiguous BF16 [B, Hkv, n_blocks, 2, D] for q [B, T, Hq, D]")
     B, T, Hq, D = q.shape
     Hkv, n_blocks = bounds.shape[1], bounds.shape[2]
-    a = _CacheArgs()
-    a.q = _tensor(q)
-    a.B, a.T, a.Hq, a.Hkv, a.D = B, T, Hq, Hkv, D
-    a.lens, a.q_lens = _ints(lens, (B,), "lens"), _ints(q_lens, (B,), "q_lens")
+    a = _CACHE_ARGS.pack(*_packed(q), *(3 * _NO_TENSOR), *_NO_SF, *_NO_SF, B, T, Hq, Hkv, D, 0,
+                         _ints(lens, (B,), "lens"), _ints(q_lens, (B,), "q_lens"), 0, 0, 0, 0, 0.0, 0)
     shape, dtype = ((B, T, Hkv, int(top)), torch.int32) if q_tile == 1 else ((B, Hkv, -(-T // 128), n_blocks), torch.uint8)
-    if out is not None and (out.dtype != dtype or tuple(out.shape) != shape or not out.is_contiguous()):
-        raise ValueError(f"out must be a contiguous {dtype} tensor of shape {list(shape)}")
+    _array(out, dtype, shape, "out")
     lib = load_library()
     with _launch(stream, q, bounds, lens, q_lens, out) as s:
         if out is None:
             out = torch.empty([max(0, n) for n in shape], dtype=dtype, device=q.device)
-        _check(lib.fmha_select_blocks(ctypes.byref(a), bounds.data_ptr(), n_blocks, int(block), int(top),
+        _check(lib.fmha_select_blocks(a, bounds.data_ptr(), n_blocks, int(block), int(top),
                                       int(sink_blocks), int(recent_blocks), int(q_tile), out.data_ptr(), s))
     return out
 
@@ -614,13 +645,13 @@ def key_weights(q, k, lse, weights, lens, q_lens=None, page_table=None, causal=T
     weights[b, h, s] (+)= sum_t sum_g exp(scale * q_tg . k_s - lse[b, g, t]), over the query heads g of KV head h
     and the tokens t that see key s. lse: contiguous fp32 [B, Hq, T] of the attention call on the same q and keys.
     q holds the last q_lens[b] (None: T) of the lens[b] tokens. Entries past lens[b] are left as they were."""
-    a = _cache_args(k, lens, page_table, q=q, q_lens=q_lens, sf_k=sf_k, softmax_scale=softmax_scale, lse=lse)
+    a, (B, Hkv, _, _) = _cache_args(k, lens, page_table, q=q, q_lens=q_lens, sf_k=sf_k, softmax_scale=softmax_scale, lse=lse)
     if weights.dim() != 3:
         raise ValueError("weights must be a contiguous float32 [B, Hkv, n] tensor")
-    w = _floats(weights, (a.B, a.Hkv, weights.shape[2]), "weights")
+    w = _floats(weights, (B, Hkv, weights.shape[2]), "weights")
     lib = load_library()
     with _launch(stream, q, k, lse, weights, lens, q_lens, page_table, *_sf_tensors(sf_k)) as s:
-        _check(lib.fmha_key_weights(ctypes.byref(a), w, weights.shape[2], 1 if causal else 0, 1 if accumulate else 0, s))
+        _check(lib.fmha_key_weights(a, w, weights.shape[2], 1 if causal else 0, 1 if accumulate else 0, s))
     return weights
 
 
@@ -633,9 +664,8 @@ def evict_select(weights, lens, budget, sinks=0, recent=0, keep=None, counts=Non
     if weights.dim() != 3:
         raise ValueError("weights must be a contiguous float32 [B, Hkv, n] tensor")
     B, Hkv, n = weights.shape
-    a = _CacheArgs()
-    a.B, a.Hkv = B, Hkv
-    a.lens = _ints(lens, (B,), "lens")
+    a = _CACHE_ARGS.pack(*(4 * _NO_TENSOR), *_NO_SF, *_NO_SF, B, 0, 0, Hkv, 0, 0, _ints(lens, (B,), "lens"),
+                         0, 0, 0, 0, 0, 0.0, 0)
     w = _floats(weights, (B, Hkv, n), "weights")
     _ints(keep, (B, Hkv, budget), "keep")
     _ints(counts, (B,), "counts")
@@ -645,7 +675,7 @@ def evict_select(weights, lens, budget, sinks=0, recent=0, keep=None, counts=Non
             keep = torch.empty((B, Hkv, max(0, budget)), dtype=torch.int32, device=weights.device)
         if counts is None:
             counts = torch.empty((B,), dtype=torch.int32, device=weights.device)
-        _check(lib.fmha_evict_select(ctypes.byref(a), w, n, int(budget), int(sinks), int(recent), keep.data_ptr(),
+        _check(lib.fmha_evict_select(a, w, n, int(budget), int(sinks), int(recent), keep.data_ptr(),
                                      counts.data_ptr(), s))
     return keep, counts
 
@@ -659,36 +689,35 @@ def cache_compact(k, v, keep, counts, dst_start=None, page_table=None, k_out=Non
     sequences. With them (and out_page_table when paged) they are copied into another cache, in any order.
     weights fp32 [B, Hkv, n] move along (to weights_out with another cache); entries past the moved ones become 0.
     Returns (k_out, v_out)."""
-    B = page_table.shape[0] if page_table is not None else k.shape[0]
     if counts is None:
         raise ValueError("counts must be a contiguous int32 tensor")
-    a = _cache_args(k, counts, page_table, v=v)
-    if keep.dtype != torch.int32 or keep.dim() != 3 or keep.shape[0] != B or keep.shape[1] not in (1, a.Hkv) or (
+    a, (B, Hkv, _, _) = _cache_args(k, counts, page_table, v=v)
+    if keep.dtype != torch.int32 or keep.dim() != 3 or keep.shape[0] != B or keep.shape[1] not in (1, Hkv) or (
             keep.shape[2] > 1 and keep.stride(2) != 1):
-        raise ValueError(f"keep must be int32 [{B}, {a.Hkv} or 1, n] with unit last stride")
+        raise ValueError(f"keep must be int32 [{B}, {Hkv} or 1, n] with unit last stride")
     start = _ints(dst_start, (B,), "dst_start")
     if (k_out is None) != (v_out is None) or (k_out is None and (out_page_table is not None or weights_out is not None)):
         raise ValueError("another cache needs k_out and v_out (and, when paged, out_page_table)")
-    o = None
+    o = 0
     if k_out is not None:
         if k_out.dtype != k.dtype or v_out.dtype != v.dtype or k_out.shape[2:] != k.shape[2:]:
             raise ValueError("k_out / v_out must have the dtypes, heads and head dim of k / v")
-        o = _cache_args(k_out, counts, out_page_table, v=v_out)
+        o, _ = _cache_args(k_out, counts, out_page_table, v=v_out)
         if (weights is None) != (weights_out is None):
             raise ValueError("weights and weights_out go together")
-    w = wo = None
+    w = wo = 0
     nw = nwo = 0
     if weights is not None:
         if weights.dim() != 3 or (weights_out is not None and weights_out.dim() != 3):
             raise ValueError("weights must be contiguous float32 [B, Hkv, n] tensors")
-        w, nw = _floats(weights, (B, a.Hkv, weights.shape[2]), "weights"), weights.shape[2]
+        w, nw = _floats(weights, (B, Hkv, weights.shape[2]), "weights"), weights.shape[2]
         wo, nwo = w, nw
         if weights_out is not None:
-            wo, nwo = _floats(weights_out, (B, a.Hkv, weights_out.shape[2]), "weights_out"), weights_out.shape[2]
+            wo, nwo = _floats(weights_out, (B, Hkv, weights_out.shape[2]), "weights_out"), weights_out.shape[2]
     lib = load_library()
     with _launch(stream, k, v, keep, counts, dst_start, page_table, k_out, v_out, out_page_table, weights,
                  weights_out) as s:
-        _check(lib.fmha_cache_compact(ctypes.byref(a), ctypes.byref(o) if o is not None else None, keep.data_ptr(),
+        _check(lib.fmha_cache_compact(a, o, keep.data_ptr(),
                                       keep.stride(0) if B > 1 else 0, keep.stride(1) if keep.shape[1] > 1 else 0,
                                       keep.shape[2], counts.data_ptr(), start, w, nw, wo, nwo, s))
     return (k, v) if k_out is None else (k_out, v_out)
