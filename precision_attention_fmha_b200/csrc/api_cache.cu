@@ -100,13 +100,29 @@ fmha_status cache_map(CUtensorMap* m, const fmha_cache_args* a, const CacheView&
                        span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
+constexpr int kPackedRows = 64;       // packed rows (T * G), and
+constexpr int kPackedKeys = 1024;     // keys of room, from which the context goes to the packed kernel
+constexpr int kPackedCtasPerSm = 3;
+
 // The sizes of an attention call that do not need the device: grid and row
 // tiles of the tree form.
 struct TreePlan {
   int rows, row_tiles, n_ctas;
+  // The context's whole 128-key tiles on the decode path's packed kernel: query-tile units of a KV head, KV splits and
+  // partial outputs (the last one is the tail's). 0 parts: the few-row kernel takes everything.
+  int units, n_splits, interleave, n_parts;
   size_t workspace_bytes;
 };
 constexpr int kMinTiles = 2;  // least key tiles of a CTA
+
+// Whether the context goes through 128-row tensor-memory tiles: many packed rows, and what that kernel is built for.
+bool tree_packed(const fmha_cache_args* a, int capacity) {
+  const int G = a->Hq / a->Hkv;
+  const int64_t rows = static_cast<int64_t>(a->T) * G;
+  return a->D == 128 && a->k.dtype == FMHA_BF16 && a->v.dtype == FMHA_BF16 && (G & (G - 1)) == 0 && G <= 128 &&
+         rows >= kPackedRows && capacity >= kPackedKeys && capacity <= 131072;
+}
+
 bool tree_plan(const fmha_cache_args* a, int capacity, TreePlan* t) {
   const int64_t packed = static_cast<int64_t>(a->T) * (a->Hq / a->Hkv);
   t->rows = cache_attn_rows(static_cast<int>(std::min<int64_t>(packed, 1 << 20)));
@@ -116,6 +132,21 @@ bool tree_plan(const fmha_cache_args* a, int capacity, TreePlan* t) {
   // Two CTAs fit an SM; more than one CTA per kMinTiles tiles has nothing to do.
   t->n_ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(2 * sm_count(), (tiles + kMinTiles - 1) / kMinTiles)));
   t->workspace_bytes = size_t(2) * t->n_ctas * t->rows * (size_t(a->D) + 1) * 4;
+  t->n_parts = 0;
+  if (tree_packed(a, capacity)) {
+    const int tiles128 = ceil_div(static_cast<int>(packed), 128);
+    t->interleave = tiles128 == 1 ? 1 : 0;
+    t->units = t->interleave ? 1 : ceil_div(tiles128, 2);
+    const int64_t base = static_cast<int64_t>(a->B) * a->Hkv * t->units;
+    const int kv = ceil_div(capacity, 128);
+    // A few CTAs per SM even out the sequences' lengths; a split keeps at least 8 tiles.
+    const int64_t want = (kPackedCtasPerSm * sm_count() + base - 1) / base;
+    t->n_splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(want, kv / 8)));
+    t->n_parts = t->n_splits * (t->interleave ? 2 : 1) + 1;
+    t->n_ctas = static_cast<int>(std::min<int64_t>(2 * sm_count(), items));
+    t->workspace_bytes = size_t(t->n_parts) * a->B * a->T * a->Hq * (size_t(a->D) + 1) * 4;
+    if (base * t->n_splits >= (int64_t(1) << 31) || static_cast<int64_t>(a->B) * a->T * a->Hq >= (int64_t(1) << 32)) return false;
+  }
   return items < (int64_t(1) << 31) && tiles / t->n_ctas < (int64_t(1) << 30);
 }
 
@@ -207,6 +238,42 @@ fmha_status fill_attn(const fmha_cache_args* a, CacheAttnParams* p, bool* k8, bo
   return cache_map(tv, a, p->c, a->v, *v8, piece, "v");
 }
 
+// The packed kernel's parameters for the contexts' whole 128-key tiles: every row sees every key of them, and every
+// tile's partial O / l and log-sum-exp go to the workspace.
+fmha_status packed_params(const fmha_cache_args* a, const CacheAttnParams& c, const TreePlan& t, AttnParams* p,
+                          CUtensorMap* tq, CUtensorMap* tk, CUtensorMap* tv) {
+  const int G = a->Hq / a->Hkv, D = a->D;
+  memset(p, 0, sizeof(*p));
+  p->B = a->B; p->Hq = a->Hq; p->Hkv = a->Hkv; p->Sq = a->T; p->Skv = c.c.capacity; p->group = G;
+  p->n_q_blocks = ceil_div(a->T, 128);
+  p->n_kv_blocks = ceil_div(c.c.capacity, 128);
+  p->scale_log2 = c.scale_log2;
+  p->packed = 1;
+  p->group_shift = log2_of(G);
+  p->n_rows = a->T * G;
+  p->n_units = t.units;
+  p->n_splits = t.n_splits;
+  p->split_tiles = ceil_div(p->n_kv_blocks, t.n_splits);
+  p->kv_interleave = t.interleave;
+  p->n_parts = t.n_parts;  // at least two: every tile writes a partial
+  p->ctx_lens = c.c.lens;
+  p->o_part = c.part_o;
+  p->lse_part = c.part_lse;
+  p->p_terms = 1;
+  p->page_table = c.c.page_table; p->num_pages = a->num_pages; p->page_size = a->page_size;
+  p->max_pages_per_seq = a->max_pages_per_seq;
+  p->err = c.c.err;
+  p->wait_cycles = c.c.wait_cycles;
+  fmha_status st;
+  const uint64_t dims[5] = {uint64_t(D), uint64_t(G), uint64_t(a->Hkv), uint64_t(a->T), uint64_t(a->B)};
+  const int64_t str[4] = {a->q.stride_h, a->q.stride_h * G, a->q.stride_s, a->q.stride_b};
+  const uint32_t box[5] = {64, uint32_t(G), 1, uint32_t(128 / G), 1};
+  if ((st = make_map_n<5>(tq, a->q.ptr, 2, dims, str, box, "q")) != FMHA_OK) return st;
+  const int rows = c.c.page_table != nullptr ? a->page_size : 128;
+  if ((st = cache_map(tk, a, c.c, a->k, false, rows, "k")) != FMHA_OK) return st;
+  return cache_map(tv, a, c.c, a->v, false, rows, "v");
+}
+
 }  // namespace
 
 extern "C" {
@@ -237,9 +304,31 @@ fmha_status fmha_fwd_tree(const fmha_cache_args* a, const uint8_t* tree_mask, in
   p.n_ctas = t.n_ctas;
   p.min_tiles = kMinTiles;
   p.part_o = static_cast<float*>(workspace);
-  p.part_lse = p.part_o + size_t(2) * t.n_ctas * t.rows * a->D;
-  cudaError_t e = launch_cache_attn(a->D, k8, v8, p, tk, tv, stream);
-  if (e == cudaSuccess) e = launch_cache_merge(a->D, p, stream);
+  cudaError_t e;
+  if (t.n_parts > 0) {
+    p.part_lse = p.part_o + size_t(t.n_parts) * a->B * a->T * a->Hq * a->D;
+    p.tail_part = t.n_parts - 1;
+    AttnParams ap;
+    CUtensorMap tq, tkp, tvp;
+    if ((st = packed_params(a, p, t, &ap, &tq, &tkp, &tvp)) != FMHA_OK) return st;
+    e = launch_attention_packed(QK_BF16, PV_BF16, p.c.page_table != nullptr, ap, tq, tkp, tvp, tq, stream);
+    if (e == cudaSuccess) e = launch_cache_tail(p, tk, tv, stream);
+    if (e == cudaSuccess) {
+      MergeParams m = {};
+      m.o_part = p.part_o;
+      m.lse_part = p.part_lse;
+      m.o = p.o;
+      m.o_sb = p.o_sb; m.o_ss = p.o_ss; m.o_sh = p.o_sh;
+      m.lse = p.lse;
+      m.n_splits = t.n_parts; m.B = a->B; m.Sq = a->T; m.Hq = a->Hq; m.D = a->D;
+      m.q_lens = p.c.q_lens;
+      e = launch_split_merge(m, stream);
+    }
+  } else {
+    p.part_lse = p.part_o + size_t(2) * t.n_ctas * t.rows * a->D;
+    e = launch_cache_attn(a->D, k8, v8, p, tk, tv, stream);
+    if (e == cudaSuccess) e = launch_cache_merge(a->D, p, stream);
+  }
   if (e != cudaSuccess) return fail(FMHA_ERR_CUDA, "tree attention launch: %s", cudaGetErrorString(e));
   return ok_status();
 }

@@ -1498,6 +1498,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int last = min(t[x].tok0 + toks - 1, p.Sq - 1) + (p.Skv - p.Sq);
         n = last < 0 ? 0 : min(p.n_kv_blocks, last / C::BN + 1);
       }
+      if (p.ctx_lens != nullptr) n = min(max(__ldg(p.ctx_lens + b), 0) / C::BN, n);
       t[x].n_kv = t[x].valid ? n : 0;
       t[x].u0 = 0;
       t[x].x = x;

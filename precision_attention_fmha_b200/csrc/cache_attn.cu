@@ -25,11 +25,12 @@
 namespace fmha {
 namespace {
 
-template <int D_, bool K8_, bool V8_, int WM_, bool PICKED_>
+template <int D_, bool K8_, bool V8_, int WM_, int MODE_>
 struct CaCfg {
   static constexpr int D = D_, WM = WM_, WN = 4 / WM_;
-  static constexpr bool K8 = K8_, V8 = V8_, PICKED = PICKED_;
-  static constexpr int MODE = PICKED ? WALK_PICKED : WALK_TREE;
+  static constexpr bool K8 = K8_, V8 = V8_;
+  static constexpr int MODE = MODE_;
+  static constexpr bool PICKED = MODE == WALK_PICKED, TAIL = MODE == WALK_TAIL;
   static constexpr bool HAS_V = true;
   using KL = TileLayout<D, K8>;
   using VL = TileLayout<D, V8>;
@@ -378,18 +379,24 @@ __device__ void consume(const CacheAttnParams& p, uint8_t* ring, float* red, CaM
         const int item_row = wmi * 16 + rr;
         const Row ro = row_of<C>(p, g, item_row);
         if (ro.tok < 0 || !ok) continue;
-        if (!whole) {
+        if constexpr (C::TAIL) {  // one partial of the row, in the layout of the packed kernel's
+          const int64_t at = ((static_cast<int64_t>(p.tail_part) * p.c.B + g.b) * p.c.T + ro.tok) * p.c.Hq + ro.head;
+          *reinterpret_cast<float4*>(p.part_o + at * D + 32 * q + 4 * c4) = v;
+        } else if (!whole) {
           *reinterpret_cast<float4*>(p.part_o + (slot * C::ROWS + item_row) * D + 32 * q + 4 * c4) = v;
         } else {
           if (!C::PICKED && ro.tok >= g.nodes) v = make_float4(0.f, 0.f, 0.f, 0.f);
           uint16_t* dst = p.o + g.b * p.o_sb + ro.tok * p.o_ss + ro.head * p.o_sh + 32 * q + 4 * c4;
           *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
         }
-        if (q == 0 && c4 == 0 && (!whole || p.lse != nullptr)) {
+        if (q == 0 && c4 == 0 && (C::TAIL || !whole || p.lse != nullptr)) {
           float M, L;
           total(wmi, rr, M, L);
           float lse = L != 0.f ? M + __log2f(L) : -INFINITY;
-          if (!whole) {
+          if constexpr (C::TAIL) {
+            p.part_lse[((static_cast<int64_t>(p.tail_part) * p.c.B + g.b) * p.c.Hq + ro.head) * p.c.T + ro.tok] =
+                lse * 0.69314718055994531f;
+          } else if (!whole) {
             p.part_lse[slot * C::ROWS + item_row] = lse;
           } else {
             if (!C::PICKED && ro.tok >= g.nodes) lse = -INFINITY;
@@ -427,6 +434,8 @@ __global__ void __launch_bounds__(C::THREADS, 2)
   if (threadIdx.x >= 128) produce<C>(p, ring, misc, &tk, &tv, w);
   else consume<C>(p, ring, red, misc, w);
   __syncthreads();
+  // The merge that follows waits for this grid alone: let it end after the packed kernel's.
+  if constexpr (C::TAIL) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Merges the partials of items that several CTAs shared, and writes the rows
@@ -528,20 +537,20 @@ cudaError_t launch_cfg(const CacheAttnParams& p, const CUtensorMap& tk, const CU
   return cudaGetLastError();
 }
 
-template <int D, bool K8, bool V8, bool PICKED>
+template <int D, bool K8, bool V8, int MODE>
 cudaError_t launch_rows(const CacheAttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
-  switch (cache_attn_rows(PICKED ? p.c.G : p.c.G * p.c.T)) {
-    case 16: return launch_cfg<CaCfg<D, K8, V8, 1, PICKED>>(p, tk, tv, s);
-    case 32: return launch_cfg<CaCfg<D, K8, V8, 2, PICKED>>(p, tk, tv, s);
-    default: return launch_cfg<CaCfg<D, K8, V8, 4, PICKED>>(p, tk, tv, s);
+  switch (cache_attn_rows(MODE == WALK_PICKED ? p.c.G : p.c.G * p.c.T)) {
+    case 16: return launch_cfg<CaCfg<D, K8, V8, 1, MODE>>(p, tk, tv, s);
+    case 32: return launch_cfg<CaCfg<D, K8, V8, 2, MODE>>(p, tk, tv, s);
+    default: return launch_cfg<CaCfg<D, K8, V8, 4, MODE>>(p, tk, tv, s);
   }
 }
 
-template <int D, bool PICKED>
+template <int D, int MODE>
 cudaError_t launch_types(bool k8, bool v8, const CacheAttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                          cudaStream_t s) {
-  if (k8) return launch_rows<D, true, true, PICKED>(p, tk, tv, s);
-  return v8 ? launch_rows<D, false, true, PICKED>(p, tk, tv, s) : launch_rows<D, false, false, PICKED>(p, tk, tv, s);
+  if (k8) return launch_rows<D, true, true, MODE>(p, tk, tv, s);
+  return v8 ? launch_rows<D, false, true, MODE>(p, tk, tv, s) : launch_rows<D, false, false, MODE>(p, tk, tv, s);
 }
 
 }  // namespace
@@ -549,8 +558,29 @@ cudaError_t launch_types(bool k8, bool v8, const CacheAttnParams& p, const CUten
 cudaError_t launch_cache_attn(int D, bool k8, bool v8, const CacheAttnParams& p, const CUtensorMap& tk,
                               const CUtensorMap& tv, cudaStream_t s) {
   if (p.blocks != nullptr)
-    return D == 64 ? launch_types<64, true>(k8, v8, p, tk, tv, s) : launch_types<128, true>(k8, v8, p, tk, tv, s);
-  return D == 64 ? launch_types<64, false>(k8, v8, p, tk, tv, s) : launch_types<128, false>(k8, v8, p, tk, tv, s);
+    return D == 64 ? launch_types<64, WALK_PICKED>(k8, v8, p, tk, tv, s)
+                   : launch_types<128, WALK_PICKED>(k8, v8, p, tk, tv, s);
+  return D == 64 ? launch_types<64, WALK_TREE>(k8, v8, p, tk, tv, s)
+                 : launch_types<128, WALK_TREE>(k8, v8, p, tk, tv, s);
+}
+
+cudaError_t launch_cache_tail(const CacheAttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+  using C = CaCfg<128, false, false, 4, WALK_TAIL>;
+  auto kern = cache_attn_kernel<C>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  // Starts on the SMs that the packed kernel's last CTAs leave free.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.n_ctas);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p, tk, tv);
 }
 
 cudaError_t launch_cache_merge(int D, const CacheAttnParams& p, cudaStream_t s) {

@@ -42,6 +42,8 @@ struct CacheAttnParams : CacheParams {
   const uint8_t* mask; int64_t mask_sb;
   float* part_o;    // [2 * n_ctas][rows per tile][D]
   float* part_lse;  // [2 * n_ctas][rows per tile], log2 units
+  // tail of a packed call: parts as the packed kernel writes them ([part][B, T, Hq, D] and [part][B, Hq, T]), its own index
+  int32_t tail_part;
 };
 
 // Rows (query token x head of the group) that one CTA takes at once: 16, 32 or 64.
@@ -49,6 +51,7 @@ inline int cache_attn_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 
 
 cudaError_t launch_cache_attn(int D, bool k8, bool v8, const CacheAttnParams& p, const CUtensorMap& tk,
                               const CUtensorMap& tv, cudaStream_t stream);
+cudaError_t launch_cache_tail(const CacheAttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream);
 cudaError_t launch_cache_merge(int D, const CacheAttnParams& p, cudaStream_t stream);
 
 // Attention weight that each cached key gathers over the query tokens.

@@ -93,6 +93,7 @@ struct Seg {
   int b, t, hkv, rt;
   int t0, t1, nt;
   int ctx, nodes;  // tree: context length and nodes in use; keys: cached tokens and query tokens in use
+  int first;       // position of tile 0's first key
   int limit;       // keys at or past it do not exist (picked: are hidden)
 };
 
@@ -109,12 +110,14 @@ __device__ __forceinline__ long long warp_sum(long long v) {
 }
 
 // What a walk goes over: a tree's context and nodes, the keys of picked blocks
-// (a fixed number of tiles per item), or all keys of a sequence.
-enum WalkMode : int { WALK_TREE = 0, WALK_PICKED = 1, WALK_KEYS = 2 };
+// (a fixed number of tiles per item), all keys of a sequence, or what the
+// packed kernel leaves of a tree's keys: the context past its last whole 128
+// keys, and the nodes (whole items only).
+enum WalkMode : int { WALK_TREE = 0, WALK_PICKED = 1, WALK_KEYS = 2, WALK_TAIL = 3 };
 
 template <int MODE>
 __device__ __forceinline__ SeqLens walk_lens(const CacheView& c, int b, bool& bad) {
-  return MODE == WALK_TREE ? tree_lens(c, b, bad) : seq_lens(c, b, bad);
+  return MODE == WALK_TREE || MODE == WALK_TAIL ? tree_lens(c, b, bad) : seq_lens(c, b, bad);
 }
 template <int MODE>
 __device__ __forceinline__ int tiles_of(const SeqLens s) {
@@ -154,6 +157,9 @@ struct Walk {
     if constexpr (MODE == WALK_PICKED) {
       pos = blockIdx.x;
       end = static_cast<long long>(p.c.B) * p.c.T * p.c.Hkv * p.row_tiles * p.n_splits;
+    } else if constexpr (MODE == WALK_TAIL) {
+      pos = blockIdx.x;
+      end = static_cast<long long>(p.c.B) * p.c.Hkv * p.row_tiles;
     } else {
       const Share s = list_share<MODE>(p, blockIdx.x == 0);
       pos = min(s.total, static_cast<long long>(blockIdx.x) * s.per);
@@ -166,6 +172,7 @@ struct Walk {
 
   __device__ bool next(const CacheParams& p, Seg& g) {
     if (pos >= end) return false;
+    g.first = 0;
     if constexpr (MODE == WALK_PICKED) {
       long long item = pos / p.n_splits;
       const int j = static_cast<int>(pos - item * p.n_splits);
@@ -185,6 +192,24 @@ struct Walk {
       g.limit = g.t < s.q ? s.len - s.q + g.t + 1 : 0;
       g.ctx = 0x7fffffff;
       g.nodes = 0;
+    } else if constexpr (MODE == WALK_TAIL) {
+      long long item = pos;
+      pos += gridDim.x;
+      g.rt = static_cast<int>(item % p.row_tiles);
+      item /= p.row_tiles;
+      g.hkv = static_cast<int>(item % p.c.Hkv);
+      g.b = static_cast<int>(item / p.c.Hkv);
+      g.t = 0;
+      bool bad;
+      const SeqLens s = walk_lens<MODE>(p.c, g.b, bad);
+      if (bad && g.hkv == 0 && g.rt == 0) atomicOr(p.c.err, kErrLength);
+      g.ctx = s.len;
+      g.nodes = s.q;
+      g.first = s.len & ~127;
+      g.limit = s.len + s.q;
+      g.nt = (g.limit - g.first + kTileKeys - 1) / kTileKeys;
+      g.t0 = 0;
+      g.t1 = g.nt;
     } else {
       const int lane = threadIdx.x & 31;
       const int items = p.c.Hkv * p.row_tiles;  // per sequence
@@ -267,7 +292,7 @@ __device__ void produce(const CacheParams& p, uint8_t* ring, RingMisc<C::STAGES>
         if (id < 0 || id >= p.n_blocks) return e;
         return cache_piece(p.c, g.b, (id << p.block_shift) + ((i & ((1 << k) - 1)) << ps), g.limit);
       } else {
-        return cache_piece(p.c, g.b, i << ps, g.limit);
+        return cache_piece(p.c, g.b, g.first + (i << ps), g.limit);
       }
     };
     int first = g.t0 * ppt;

@@ -69,6 +69,9 @@ struct AttnParams {
   // tiles hold the same rows and take alternate kept KV tiles of the split;
   // each is then its own partial (n_parts = 2 * n_splits), else n_parts = n_splits.
   int32_t n_splits, split_tiles, kv_interleave, n_parts;
+  // Packed, nullable [B]: sequence b has only its first ctx_lens[b] / 128 whole
+  // key tiles here (the rest is another kernel's); Skv then bounds them all.
+  const int32_t* ctx_lens;
   float* o_part;   // [n_parts, B, Sq, Hq, D] when n_parts > 1
   float* lse_part; // [n_parts, B, Hq, Sq]
   uint32_t* err;        // device error word
@@ -109,6 +112,7 @@ struct MergeParams {
   uint16_t* o; int64_t o_sb, o_ss, o_sh;  // bf16 bits
   float* lse;                             // nullable [B, Hq, Sq]
   int32_t n_splits, B, Sq, Hq, D;
+  const int32_t* q_lens;                  // nullable [B]: rows of later tokens give O = 0, lse = -inf
 };
 cudaError_t launch_split_merge(const MergeParams& m, cudaStream_t stream);
 
