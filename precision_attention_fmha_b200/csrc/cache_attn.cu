@@ -16,25 +16,30 @@
 // log-sum-exp go to the workspace and a second kernel merges them.
 //
 // 160 threads: four MMA warps and one TMA producer warp feeding a ring of
-// 64-key slots. A warp takes 16 rows; with at most 16 rows the four warps take
-// 16 keys of the slot each (own m, l, O, joined at the item's end), with 32
-// rows two and two, with 64 rows every warp takes all keys.
+// 64-key slots.
+//  - At most 16 rows (consume_t): the four warps take 16 keys of the slot each
+//    (own m, l, O, joined at the item's end) and compute S^T = K Q^T and
+//    O^T = V^T P^T, so the keys and the head dim fill the instructions' 16-row
+//    side and 8 or 16 query rows their 8-column side.
+//  - More rows (consume): a warp takes 16 rows, S = Q K^T and O = P V; with 32
+//    rows two warps share the slot's keys, with 64 every warp takes all keys.
 #include "cache_tiles.cuh"
 #include "mma_sync.cuh"
 
 namespace fmha {
 namespace {
 
-template <int D_, bool K8_, bool V8_, int WM_, int MODE_>
+template <int D_, bool K8_, bool V8_, int ROWS_, int MODE_>
 struct CaCfg {
-  static constexpr int D = D_, WM = WM_, WN = 4 / WM_;
+  static constexpr int D = D_, ROWS = ROWS_;
+  static constexpr int NT = ROWS <= 16 ? ROWS / 8 : 0;   // transposed: 8-column tiles of query rows
+  static constexpr int WM = NT ? 1 : ROWS / 16, WN = 4 / WM;
   static constexpr bool K8 = K8_, V8 = V8_;
   static constexpr int MODE = MODE_;
   static constexpr bool PICKED = MODE == WALK_PICKED, TAIL = MODE == WALK_TAIL;
   static constexpr bool HAS_V = true;
   using KL = TileLayout<D, K8>;
   using VL = TileLayout<D, V8>;
-  static constexpr int ROWS = 16 * WM;
   static constexpr int SLOT = KL::BYTES + VL::BYTES;
   static constexpr int STAGES = SLOT >= 32768 ? 3 : SLOT >= 24576 ? 4 : SLOT >= 16384 ? 6 : 8;
   static constexpr int RED_LD = 36;  // floats per row of the joining buffer (32 columns + padding)
@@ -135,7 +140,7 @@ __device__ void consume(const CacheAttnParams& p, uint8_t* ring, float* red, CaM
     for (int h = 0; h < 2; ++h) {
       rows[h] = row_of<C>(p, g, wm * 16 + gq + 8 * h);
       const uint16_t* src = p.q + g.b * p.q_sb + rows[h].tok * p.q_ss + rows[h].head * p.q_sh;
-      load_q<C::K8, KS>(qf, h, cs[h], src, rows[h].tok >= 0, j);
+      load_q<C::K8, KS, 4>(qf, h, cs[h], src, rows[h].tok >= 0, j);
       cs[h] *= p.scale_log2 * sfk;
     }
     float acc[NQ * 4][4];
@@ -175,10 +180,7 @@ __device__ void consume(const CacheAttnParams& p, uint8_t* ring, float* red, CaM
             for (int s2 = 0; s2 < KS / 2; ++s2) {
               uint32_t r[4];
               ldsm4(r, k_base + C::KL::at(row, 2 * s2 + ((lane >> 3) & 1)));
-#pragma unroll
-              for (int e = 0; e < 4; ++e)  // e: which 16 columns (bit 0), which 8 keys (bit 1)
-                mma_f16(sc[2 * i + (e >> 1)], qf[2 * s2 + (e & 1)], e4m3x2_to_f16x2(r[e] & 0xffffu),
-                        e4m3x2_to_f16x2(r[e] >> 16));
+              mma_k8<KS>(sc[2 * i], sc[2 * i + 1], qf, s2, r);
             }
           } else {
 #pragma unroll
@@ -192,21 +194,29 @@ __device__ void consume(const CacheAttnParams& p, uint8_t* ring, float* red, CaM
         }
         if (!plain) {  // hide keys: past the end, or nodes this row does not see
 #pragma unroll
-          for (int i = 0; i < GPW * 2; ++i)
+          for (int i = 0; i < GPW; ++i) {
+            uint32_t show = 0xffu;  // bit 4 x + e of the group's sc[2 i + x][e]
+            if constexpr (!C::PICKED) {
+              const int node0 = pos[i] - g.ctx;  // node of the group's first key
+              if (node0 + 16 > 0) {
+                show = 0u;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int k = (i & 1) * 8 + 2 * j + (e & 1);  // key inside the group
-              bool see = k < valid[i >> 1];
-              if constexpr (!C::PICKED) {
-                const int node = pos[i >> 1] + k - g.ctx;
-                const int tok = rows[e >> 1].tok;
-                if (see && node >= 0)
-                  see = tok >= 0 && (p.mask == nullptr
-                                         ? node <= tok
-                                         : p.mask[g.b * p.mask_sb + static_cast<int64_t>(tok) * p.c.T + node] != 0);
+                for (int e = 0; e < 8; ++e) {  // all loads first: one latency per group, not one per key
+                  const int node = node0 + (e >> 2) * 8 + 2 * j + (e & 1), tok = rows[(e >> 1) & 1].tok;
+                  bool see = node < 0 || (tok >= 0 && node <= tok);
+                  if (p.mask != nullptr) {
+                    const uint8_t byte = __ldg(p.mask + g.b * p.mask_sb + static_cast<int64_t>(max(tok, 0)) * p.c.T +
+                                               min(max(node, 0), p.c.T - 1));
+                    see = node < 0 || (tok >= 0 && byte != 0);
+                  }
+                  show |= see ? 1u << e : 0u;
+                }
               }
-              if (!see) sc[i][e] = -INFINITY;
             }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if ((e >> 2) * 8 + 2 * j + (e & 1) >= valid[i] || !((show >> e) & 1u)) sc[2 * i + (e >> 2)][e & 3] = -INFINITY;
+          }
         }
         // Running maximum, exponentials and row sums.
         float mb[2];
@@ -410,6 +420,349 @@ __device__ void consume(const CacheAttnParams& p, uint8_t* ring, float* red, CaM
   }
 }
 
+// 8x8 transpose of a 16-bit matrix across the warp: lane (g, j) holds row g, columns 2 j, 2 j + 1.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// K fragments as the 16-row side (16 keys): k-steps 2 s and 2 s + 1 (E4M3), or s (BF16).
+template <class C>
+__device__ __forceinline__ void load_kt(uint32_t (&a)[C::K8 ? 2 : 1][4], uint32_t k_base, int key0, int s, int lane) {
+  using namespace ptx;
+  uint32_t r[4];
+  ldsm4(r, k_base + C::KL::at(key0 + (lane & 15), 2 * s + (lane >> 4)));
+  if constexpr (C::K8) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      a[h][0] = e4m3x2_to_f16x2(r[2 * h] & 0xffffu);
+      a[h][1] = e4m3x2_to_f16x2(r[2 * h + 1] & 0xffffu);
+      a[h][2] = e4m3x2_to_f16x2(r[2 * h] >> 16);
+      a[h][3] = e4m3x2_to_f16x2(r[2 * h + 1] >> 16);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[0][i] = r[i];
+  }
+}
+
+// V^T fragments of columns 32 q .. 32 q + 31 (two 16-row tiles) x 16 keys.
+// BF16: tile h is columns 32 q + 16 h ..; E4M3: rows g and g + 8 of tile h are
+// columns 32 q + 4 g + 2 h and + 1 (a word holds four neighbouring columns).
+template <class C>
+__device__ __forceinline__ void load_vt(uint32_t (&a)[2][4], uint32_t v_base, int key0, int q, int lane) {
+  using namespace ptx;
+  if constexpr (C::V8) {
+    const int g = lane >> 2, j = lane & 3;
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = lds32(v_base + C::VL::at(key0 + 2 * j + (i & 1) + 8 * (i >> 1), 2 * q + (g >> 2)) + (g & 3) * 4);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t lo = __byte_perm(w[2 * k], w[2 * k + 1], 0x5140), hi = __byte_perm(w[2 * k], w[2 * k + 1], 0x7362);
+      a[0][2 * k] = e4m3x2_to_f16x2(lo & 0xffffu);
+      a[0][2 * k + 1] = e4m3x2_to_f16x2(lo >> 16);
+      a[1][2 * k] = e4m3x2_to_f16x2(hi & 0xffffu);
+      a[1][2 * k + 1] = e4m3x2_to_f16x2(hi >> 16);
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // matrices: keys 0-7 | 8-15 (bit 4 of the lane) x columns 0-7 | 8-15 (bit 3)
+      const int row = key0 + (lane & 7) + ((lane >> 4) & 1) * 8;
+      ldsm4t(a[h], v_base + C::VL::at(row, 4 * q + 2 * h + ((lane >> 3) & 1)));
+    }
+  }
+}
+
+template <class C>
+__device__ void consume_t(const CacheAttnParams& p, uint8_t* ring, float* red, CaMisc<C::STAGES>* misc, const Waiter w) {
+  using namespace ptx;
+  constexpr int D = C::D, KS = D / 16, NQ = D / 32, NT = C::NT;
+  constexpr float kTau = 8.f;  // the running maximum moves when it is exceeded by more than 2^8 (weights stay below it)
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gq = lane >> 2, j = lane & 3;
+  uint32_t it = 0;
+  bool ok = true;
+  Walk<C::MODE> walk;
+  walk.start(p);
+  Seg g;
+  while (walk.next(p, g)) {
+    const int64_t bh = g.b * static_cast<int64_t>(p.c.Hkv) + g.hkv;
+    const float sfk = sf_of(p.sf_k, p.sf_k_kind, bh), sfv = sf_of(p.sf_v, p.sf_v_kind, bh);
+    // Q^T fragments: query row 8 n + gq of each tile; the score factors and tokens of rows 8 n + 2 j and + 1.
+    uint32_t qf[NT][KS][2];
+    float cs[NT][2];
+    int tok[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const Row ro = row_of<C>(p, g, 8 * n + gq);
+      float f;
+      load_q<C::K8, KS, 2>(qf[n], 0, f, p.q + g.b * p.q_sb + ro.tok * p.q_ss + ro.head * p.q_sh, ro.tok >= 0, j);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        cs[n][e] = p.scale_log2 * sfk * __shfl_sync(kFull, f, 4 * (2 * j + e));
+        tok[n][e] = __shfl_sync(kFull, ro.tok, 4 * (2 * j + e));
+      }
+    }
+    float acc[NT][2 * NQ][4];
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int i = 0; i < 2 * NQ; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[n][i][e] = 0.f;
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+    }
+    const int key0 = warp * 16;
+
+    for (int u = g.t0; u < g.t1 && ok; ++u) {
+      const int s = it % C::STAGES;
+      ok = __all_sync(kFull, w.wait(smem_addr(&misc->full[s]), (it / C::STAGES) & 1));
+      if (!ok) break;
+      ++it;
+      const uint32_t k_base = smem_addr(ring + s * C::SLOT), v_base = k_base + C::KL::BYTES;
+      const int valid = misc->meta[s].valid[warp], pos = misc->meta[s].pos[warp];
+      const bool plain = valid == 16 && pos + 16 <= g.ctx;
+      if (valid > 0) {
+        // S^T: sc[n][e] is key gq + 8 (e >> 1), query row 8 n + 2 j + (e & 1). Two chains per tile.
+        float sc[NT][4], s2[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[n][e] = s2[n][e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < (C::K8 ? KS / 2 : KS); ++k) {
+          uint32_t a[C::K8 ? 2 : 1][4];
+          load_kt<C>(a, k_base, key0, k, lane);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if constexpr (C::K8) {
+              mma_f16(sc[n], a[0], qf[n][2 * k][0], qf[n][2 * k][1]);
+              mma_f16(s2[n], a[1], qf[n][2 * k + 1][0], qf[n][2 * k + 1][1]);
+            } else {
+              mma_bf16(k & 1 ? s2[n] : sc[n], a[0], qf[n][k][0], qf[n][k][1]);
+            }
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[n][e] += s2[n][e];
+        if (!plain) {  // hide keys: past the end, or nodes this row does not see
+          uint32_t show = kFull;
+          if constexpr (!C::PICKED) {
+            const int node0 = pos - g.ctx;  // node of the group's first key
+            if (node0 + 16 > 0) {
+              show = 0u;
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int node = node0 + gq + 8 * (e >> 1), t = tok[n][e & 1];
+                  bool see = node < 0 || (t >= 0 && node <= t);
+                  if (p.mask != nullptr) {
+                    const uint8_t byte = __ldg(p.mask + g.b * p.mask_sb + static_cast<int64_t>(max(t, 0)) * p.c.T +
+                                               min(max(node, 0), p.c.T - 1));
+                    see = node < 0 || (t >= 0 && byte != 0);
+                  }
+                  show |= see ? 1u << (4 * n + e) : 0u;
+                }
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (gq + 8 * (e >> 1) >= valid || !((show >> (4 * n + e)) & 1u)) sc[n][e] = -INFINITY;
+        }
+        // The running maximum is lazy: usually one vote says that it stays.
+        bool over = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) over = over || fmaxf(sc[n][e], sc[n][2 + e]) * cs[n][e] > m[n][e] + kTau;
+        if (__any_sync(kFull, over)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float mx = fmaxf(sc[n][e], sc[n][2 + e]) * cs[n][e];
+              mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
+              const float mn = fmaxf(m[n][e], mx);
+              const float f = mn > m[n][e] ? ex2(m[n][e] - mn) : 1.f;
+              m[n][e] = mn;
+              l[n][e] *= f;
+#pragma unroll
+              for (int i = 0; i < 2 * NQ; ++i) {
+                acc[n][i][e] *= f;
+                acc[n][i][2 + e] *= f;
+              }
+            }
+        }
+        uint32_t x[NT][2], pb[NT][2];
+        uint32_t seen = 0;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float e4[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (!plain && sc[n][e] != -INFINITY) seen |= 1u << (4 * n + e);
+            e4[e] = ex2(fmaf(sc[n][e], cs[n][e & 1], m[n][e & 1] == -INFINITY ? 0.f : -m[n][e & 1]));
+            l[n][e & 1] += e4[e];
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            x[n][h] = pack_p<C>(e4[2 * h], e4[2 * h + 1]);
+            pb[n][h] = transpose8(x[n][h]);
+          }
+        }
+        // O^T += V^T P^T.
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+          uint32_t a[2][4];
+          load_vt<C>(a, v_base, key0, q, lane);
+          if (!plain) {
+            // Rows past the end hold anything: they count as zero. A node
+            // that some row does not see may hold infinities or NaN, which a
+            // zero weight would not stop: such a group adds key by key.
+            uint32_t keep[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              keep[h] = (2 * j + 8 * h < valid ? 0xffffu : 0u) | (2 * j + 1 + 8 * h < valid ? 0xffff0000u : 0u);
+            bool odd = false;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                a[t][i] &= keep[i >> 1];
+                odd = odd || not_finite<C::V8>(a[t][i]);
+              }
+            if (__any_sync(kFull, odd)) {
+#pragma unroll 1
+              for (int k = 0; k < 16; ++k) {
+                const int from_p = (k & 7) * 4 + j, from_v = (lane & ~3) | ((k & 7) >> 1);
+                const uint32_t sb = __shfl_sync(kFull, seen, from_p) >> (2 * (k >> 3));
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                  const uint32_t x0 = __shfl_sync(kFull, x[n][0], from_p), x1 = __shfl_sync(kFull, x[n][1], from_p);
+                  const uint32_t xk = k < 8 ? x0 : x1;
+                  const float p0 = half_of<C::V8>(xk, 0), p1 = half_of<C::V8>(xk, 1);
+                  const bool s0 = (sb >> (4 * n)) & 1u, s1 = (sb >> (4 * n + 1)) & 1u;
+#pragma unroll
+                  for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {  // column rows gq and gq + 8
+                      const uint32_t v0 = __shfl_sync(kFull, a[t][h], from_v), v1 = __shfl_sync(kFull, a[t][2 + h], from_v);
+                      const float v = half_of<C::V8>(k < 8 ? v0 : v1, k & 1);
+                      if (s0) acc[n][2 * q + t][2 * h] = fmaf(p0, v, acc[n][2 * q + t][2 * h]);
+                      if (s1) acc[n][2 * q + t][2 * h + 1] = fmaf(p1, v, acc[n][2 * q + t][2 * h + 1]);
+                    }
+                }
+              }
+              continue;
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if constexpr (C::V8) mma_f16(acc[n][2 * q + t], a[t], pb[n][0], pb[n][1]);
+              else mma_bf16(acc[n][2 * q + t], a[t], pb[n][0], pb[n][1]);
+            }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&misc->empty[s]));
+    }
+
+    // Join the four warps, and write O / l (or a partial).
+    named_bar_sync(1, 128);  // the last item's (m, l) have been read
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[n][e] += __shfl_xor_sync(kFull, l[n][e], 4);
+        l[n][e] += __shfl_xor_sync(kFull, l[n][e], 8);
+        l[n][e] += __shfl_xor_sync(kFull, l[n][e], 16);
+        if (gq == 0) {
+          misc->ml[warp][8 * n + 2 * j + e][0] = m[n][e];
+          misc->ml[warp][8 * n + 2 * j + e][1] = l[n][e];
+        }
+      }
+    named_bar_sync(1, 128);
+    auto total = [&](int r, float& M, float& L) {
+      M = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) M = fmaxf(M, misc->ml[x][r][0]);
+      const float Mb = M == -INFINITY ? 0.f : M;
+      L = 0.f;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) L += misc->ml[x][r][1] * ex2(misc->ml[x][r][0] - Mb);
+    };
+    float f[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float M, L;
+        total(8 * n + 2 * j + e, M, L);
+        f[n][e] = L != 0.f ? ex2(m[n][e] - (M == -INFINITY ? 0.f : M)) * (sfv / L) : 0.f;
+      }
+    const int r = threadIdx.x / 8, c4 = threadIdx.x % 8;  // 8 lanes per row write
+    const Row ro = row_of<C>(p, g, r);
+    const bool mine = r < C::ROWS && ro.tok >= 0 && ok;
+    const bool whole = g.t0 == 0 && g.t1 == g.nt;
+    const int64_t slot = 2ll * blockIdx.x + (g.t0 == 0 ? 1 : 0);
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int col = C::V8 ? 4 * gq + 2 * t + (e >> 1) : 16 * t + gq + 8 * (e >> 1);
+            red[(warp * 16 + 8 * n + 2 * j + (e & 1)) * C::RED_LD + col] = acc[n][2 * q + t][e] * f[n][e & 1];
+          }
+      named_bar_sync(1, 128);
+      if (mine) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float4 y = *reinterpret_cast<const float4*>(red + (x * 16 + r) * C::RED_LD + 4 * c4);
+          v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
+        }
+        if (!whole) {
+          *reinterpret_cast<float4*>(p.part_o + (slot * C::ROWS + r) * D + 32 * q + 4 * c4) = v;
+        } else {
+          if (!C::PICKED && ro.tok >= g.nodes) v = make_float4(0.f, 0.f, 0.f, 0.f);
+          uint16_t* dst = p.o + g.b * p.o_sb + ro.tok * p.o_ss + ro.head * p.o_sh + 32 * q + 4 * c4;
+          *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        }
+      }
+      named_bar_sync(1, 128);
+    }
+    if (mine && c4 == 0 && (!whole || p.lse != nullptr)) {
+      float M, L;
+      total(r, M, L);
+      float lse = L != 0.f ? M + __log2f(L) : -INFINITY;
+      if (!whole) {
+        p.part_lse[slot * C::ROWS + r] = lse;
+      } else {
+        if (!C::PICKED && ro.tok >= g.nodes) lse = -INFINITY;
+        p.lse[(static_cast<int64_t>(g.b) * p.c.Hq + ro.head) * p.c.T + ro.tok] = lse * 0.69314718055994531f;
+      }
+    }
+  }
+}
+
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 2)
     cache_attn_kernel(const __grid_constant__ CacheAttnParams p, const __grid_constant__ CUtensorMap tk,
@@ -432,6 +785,7 @@ __global__ void __launch_bounds__(C::THREADS, 2)
   __syncthreads();
   const Waiter w{&misc->abort, p.c.err, p.c.wait_cycles};
   if (threadIdx.x >= 128) produce<C>(p, ring, misc, &tk, &tv, w);
+  else if constexpr (C::NT > 0) consume_t<C>(p, ring, red, misc, w);
   else consume<C>(p, ring, red, misc, w);
   __syncthreads();
   // The merge that follows waits for this grid alone: let it end after the packed kernel's.
@@ -540,9 +894,10 @@ cudaError_t launch_cfg(const CacheAttnParams& p, const CUtensorMap& tk, const CU
 template <int D, bool K8, bool V8, int MODE>
 cudaError_t launch_rows(const CacheAttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
   switch (cache_attn_rows(MODE == WALK_PICKED ? p.c.G : p.c.G * p.c.T)) {
-    case 16: return launch_cfg<CaCfg<D, K8, V8, 1, MODE>>(p, tk, tv, s);
-    case 32: return launch_cfg<CaCfg<D, K8, V8, 2, MODE>>(p, tk, tv, s);
-    default: return launch_cfg<CaCfg<D, K8, V8, 4, MODE>>(p, tk, tv, s);
+    case 8: return launch_cfg<CaCfg<D, K8, V8, 8, MODE>>(p, tk, tv, s);
+    case 16: return launch_cfg<CaCfg<D, K8, V8, 16, MODE>>(p, tk, tv, s);
+    case 32: return launch_cfg<CaCfg<D, K8, V8, 32, MODE>>(p, tk, tv, s);
+    default: return launch_cfg<CaCfg<D, K8, V8, 64, MODE>>(p, tk, tv, s);
   }
 }
 
@@ -565,7 +920,7 @@ cudaError_t launch_cache_attn(int D, bool k8, bool v8, const CacheAttnParams& p,
 }
 
 cudaError_t launch_cache_tail(const CacheAttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
-  using C = CaCfg<128, false, false, 4, WALK_TAIL>;
+  using C = CaCfg<128, false, false, 64, WALK_TAIL>;
   auto kern = cache_attn_kernel<C>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;

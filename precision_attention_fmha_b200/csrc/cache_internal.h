@@ -46,8 +46,8 @@ struct CacheAttnParams : CacheParams {
   int32_t tail_part;
 };
 
-// Rows (query token x head of the group) that one CTA takes at once: 16, 32 or 64.
-inline int cache_attn_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+// Rows (query token x head of the group) that one CTA takes at once.
+inline int cache_attn_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 cudaError_t launch_cache_attn(int D, bool k8, bool v8, const CacheAttnParams& p, const CUtensorMap& tk,
                               const CUtensorMap& tv, cudaStream_t stream);

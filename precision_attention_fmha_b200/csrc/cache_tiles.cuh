@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 
 #include "cache_internal.h"
+#include "mma_sync.cuh"
 #include "ptx_sm100.cuh"
 #include "waiter.cuh"
 
@@ -359,6 +360,15 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t v) {
   return ptx::pack_bf16x2(f.x, f.y);
 }
 
+// Scores of 16 queries x 16 keys, 32 columns (k-steps 2 s and 2 s + 1), from a fragment load of K's codes.
+template <int KS>
+__device__ __forceinline__ void mma_k8(float (&s0)[4], float (&s1)[4], const uint32_t (&qf)[KS][4], int s,
+                                       const uint32_t (&r)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e)  // e: which 16 columns (bit 0), which 8 keys (bit 1)
+    ptx::mma_f16(e & 2 ? s1 : s0, qf[2 * s + (e & 1)], ptx::e4m3x2_to_f16x2(r[e] & 0xffffu), ptx::e4m3x2_to_f16x2(r[e] >> 16));
+}
+
 // Row h (0: gq, 1: gq + 8) of the 16 x D query fragment of a warp, from D
 // BF16 values at src (live false: zeros), and the factor that its scores take.
 // For E4M3 keys the contraction runs in F16, which holds the codes exactly: the
@@ -366,8 +376,9 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t v) {
 // values 2^-14 of the row's largest and smaller, which keep an absolute error
 // of 2^-25 of it; and the columns of a fragment are those whose codes one
 // 32-bit word of K holds (4 j .. 4 j + 3 of each 16).
-template <bool K8, int KS>
-__device__ __forceinline__ void load_q(uint32_t (&qf)[KS][4], int h, float& factor, const uint16_t* src, bool live,
+// N = 4: row h of the 16-row side; N = 2: the 8-column side (h = 0, one row per lane group).
+template <bool K8, int KS, int N>
+__device__ __forceinline__ void load_q(uint32_t (&qf)[KS][N], int h, float& factor, const uint16_t* src, bool live,
                                        int j) {
   if constexpr (K8) {
     uint32_t raw[KS][2];
@@ -393,14 +404,14 @@ __device__ __forceinline__ void load_q(uint32_t (&qf)[KS][4], int h, float& fact
     for (int s = 0; s < KS; ++s)
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        qf[s][h + 2 * e] = ptx::pack_f16x2(half_of<false>(raw[s][e], 0) * down, half_of<false>(raw[s][e], 1) * down);
+        qf[s][h + N / 2 * e] = ptx::pack_f16x2(half_of<false>(raw[s][e], 0) * down, half_of<false>(raw[s][e], 1) * down);
   } else {
     factor = 1.f;
 #pragma unroll
     for (int s = 0; s < KS; ++s)
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        qf[s][h + 2 * e] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * s + 8 * e + 2 * j)) : 0u;
+        qf[s][h + N / 2 * e] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * s + 8 * e + 2 * j)) : 0u;
   }
 }
 

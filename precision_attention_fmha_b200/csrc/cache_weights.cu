@@ -57,12 +57,26 @@ __device__ void weigh(const KeyWeightsParams& p, uint8_t* ring, RingMisc<C::STAG
         const bool live = t < g.nodes;  // token rows in use (r < rows follows: nodes <= T)
         at[h] = g.ctx - g.nodes + t;
         nl[h] = live ? neg_lse2(__ldg(p.lse + (static_cast<int64_t>(g.b) * p.c.Hq + head) * p.c.T + t)) : -INFINITY;
-        load_q<C::K8, KS>(qf, h, cs[h], p.q + g.b * p.q_sb + static_cast<int64_t>(t) * p.q_ss + head * p.q_sh, live, j);
+        load_q<C::K8, KS, 4>(qf, h, cs[h], p.q + g.b * p.q_sb + static_cast<int64_t>(t) * p.q_ss + head * p.q_sh, live, j);
         cs[h] *= c0;
       }
     };
     if (tiles == 1) load_rows(0);
+    // Lanes of the first row group hold the sums of keys 2 j, 2 j + 1, 2 j + 8, 2 j + 9; what the weights held is
+    // fetched one tile ahead (the load's latency in every tile was two thirds of a decoding step's time).
+    auto fetch = [&](int u, float (&x)[4]) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int key = u * kTileKeys + warp * 16 + 8 * (e >> 1) + 2 * j + (e & 1);
+        x[e] = p.accumulate && gq == 0 && u < g.t1 && key < min(g.limit, p.n_weights) ? p.weights[bh * p.n_weights + key] : 0.f;
+      }
+    };
+    float old[4], ahead[4];
+    fetch(g.t0, ahead);
     for (int u = g.t0; u < g.t1; ++u) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) old[e] = ahead[e];
+      fetch(u + 1, ahead);
       const int s = it % C::STAGES;
       ok = __all_sync(kFull, w.wait(smem_addr(&misc->full[s]), (it / C::STAGES) & 1));
       if (!ok) break;
@@ -85,9 +99,7 @@ __device__ void weigh(const KeyWeightsParams& p, uint8_t* ring, RingMisc<C::STAG
 #pragma unroll
         for (int i = 0; i < KS; ++i) {
           if constexpr (C::K8) {
-            const uint32_t a = kb[i / 2][i & 1], b = kb[i / 2][2 + (i & 1)];
-            mma_f16(sc[0], qf[i], e4m3x2_to_f16x2(a & 0xffffu), e4m3x2_to_f16x2(a >> 16));
-            mma_f16(sc[1], qf[i], e4m3x2_to_f16x2(b & 0xffffu), e4m3x2_to_f16x2(b >> 16));
+            if (i % 2 == 0) mma_k8<KS>(sc[0], sc[1], qf, i / 2, kb[i / 2]);
           } else {
             mma_bf16(sc[0], qf[i], kb[i][0], kb[i][1]);
             mma_bf16(sc[1], qf[i], kb[i][2], kb[i][3]);
@@ -112,10 +124,7 @@ __device__ void weigh(const KeyWeightsParams& p, uint8_t* ring, RingMisc<C::STAG
           v += __shfl_xor_sync(kFull, v, 8);
           v += __shfl_xor_sync(kFull, v, 16);
           const int k = 8 * i + 2 * j + e;
-          if (gq == 0 && k < valid && pos + k < p.n_weights) {
-            float* dst = p.weights + bh * p.n_weights + pos + k;
-            *dst = p.accumulate ? *dst + v : v;
-          }
+          if (gq == 0 && k < valid && pos + k < p.n_weights) p.weights[bh * p.n_weights + pos + k] = old[2 * i + e] + v;
         }
     }
   }

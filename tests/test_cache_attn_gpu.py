@@ -192,3 +192,21 @@ def test_selected(B, T, Hq, Hkv, D, lens, block, top, page, kv):
     o = fmha.fmha_fwd_selected(q, k, v, blocks, i32(lens), block, q_lens, table, sf_k=sf[0], sf_v=sf[1], lse=lse)
     fmha.get_device_error()
     ref.check(o, lse, ref.selected(q, k, v, blocks, lens, block, q_lens, table, *sf), v8=kv != "bf16")
+
+
+def test_tree_e4m3_visible_nan_codes_reach_their_rows():
+    """NaN codes of K and V that a row sees make it NaN (V: that column); rows that do not see them are untouched."""
+    from precision_attention_fmha_b200 import fmha
+
+    q, k, v, sf, g = make(8, 1, 4, 4, 2, 128, 64, 0, "e4m3")
+    nan = torch.full((1,), float("nan"), device=DEV).to(k.dtype)
+    k[0, 30, 0] = nan       # node 0, KV head 0
+    v[0, 31, 1, 5] = nan    # node 1, KV head 1, one column
+    mask = torch.eye(4, device=DEV, dtype=torch.uint8)[None].contiguous()
+    lse = torch.empty(1, 4, 4, device=DEV)
+    o = fmha.fmha_fwd_tree(q, k, v, i32([30]), mask, lse=lse, sf_k=sf[0], sf_v=sf[1])
+    assert torch.isnan(o[0, 0, :2]).all() and torch.isnan(lse[0, :2, 0]).all()
+    assert torch.isnan(o[0, 1, 2:, 5]).all()
+    o[0, 0, :2], o[0, 1, 2:, 5] = 0, 0
+    lse[0, :2, 0] = 0
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
