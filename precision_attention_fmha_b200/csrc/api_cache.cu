@@ -96,8 +96,13 @@ fmha_status cache_map(CUtensorMap* m, const fmha_cache_args* a, const CacheView&
                             uint64_t(paged ? a->num_pages : a->B)};
   const int64_t strides[3] = {t.stride_h, t.stride_s, t.stride_b};
   const uint32_t box[4] = {uint32_t(span / eb), 1, uint32_t(rows), 1};
+  // L2 fetches no more than one head's row of a token: the neighbouring head's belongs to another CTA, and by the time
+  // that one asks it is gone (E4M3, D = 128, 256-byte fetches: 600 MB read from DRAM for 452).
+  const int row = a->D * eb;
   return make_map_n<4>(m, t.ptr, eb, dims, strides, box, what,
-                       span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+                       span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                       row >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                  : row >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B);
 }
 
 constexpr int kPackedRows = 64;       // packed rows (T * G), and
@@ -129,8 +134,8 @@ bool tree_plan(const fmha_cache_args* a, int capacity, TreePlan* t) {
   t->row_tiles = static_cast<int>((packed + t->rows - 1) / t->rows);
   const int64_t items = static_cast<int64_t>(a->B) * a->Hkv * t->row_tiles;
   const int64_t tiles = items * ceil_div(std::max(capacity, 1), kTile);
-  // Two CTAs fit an SM; more than one CTA per kMinTiles tiles has nothing to do.
-  t->n_ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(2 * sm_count(), (tiles + kMinTiles - 1) / kMinTiles)));
+  // More than one CTA per kMinTiles tiles has nothing to do.
+  t->n_ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(cache_attn_ctas(t->rows) * sm_count(), (tiles + kMinTiles - 1) / kMinTiles)));
   t->workspace_bytes = size_t(2) * t->n_ctas * t->rows * (size_t(a->D) + 1) * 4;
   t->n_parts = 0;
   if (tree_packed(a, capacity)) {
@@ -160,7 +165,7 @@ bool pick_plan(const fmha_cache_args* a, int top, int block, PickPlan* t) {
   t->row_tiles = ceil_div(G, t->rows);
   const int64_t items = static_cast<int64_t>(a->B) * a->T * a->Hkv * t->row_tiles;
   t->item_tiles = static_cast<int>((static_cast<int64_t>(top) * block + kTile - 1) / kTile);
-  const int target = 2 * sm_count();
+  const int target = cache_attn_ctas(t->rows) * sm_count();
   int splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(target / std::max<int64_t>(1, items), t->item_tiles)));
   t->per_split = ceil_div(t->item_tiles, splits);
   t->n_splits = ceil_div(t->item_tiles, t->per_split);

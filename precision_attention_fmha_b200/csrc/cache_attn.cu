@@ -41,7 +41,10 @@ struct CaCfg {
   using KL = TileLayout<D, K8>;
   using VL = TileLayout<D, V8>;
   static constexpr int SLOT = KL::BYTES + VL::BYTES;
-  static constexpr int STAGES = SLOT >= 32768 ? 3 : SLOT >= 24576 ? 4 : SLOT >= 16384 ? 6 : 8;
+  // CTAs that share an SM, and ring slots in what shared memory each has.
+  static constexpr int CTAS = cache_attn_ctas(ROWS);
+  static constexpr int STAGES_FIT = ((CTAS == 3 ? 76800 : 114688) - 9216 - 2048) / SLOT;
+  static constexpr int STAGES = STAGES_FIT > 8 ? 8 : STAGES_FIT;
   static constexpr int RED_LD = 36;  // floats per row of the joining buffer (32 columns + padding)
   static constexpr int RED_BYTES = 4 * 16 * RED_LD * 4;
   static constexpr int SMEM = STAGES * SLOT + RED_BYTES + 2048;
@@ -764,7 +767,7 @@ __device__ void consume_t(const CacheAttnParams& p, uint8_t* ring, float* red, C
 }
 
 template <class C>
-__global__ void __launch_bounds__(C::THREADS, 2)
+__global__ void __launch_bounds__(C::THREADS, C::CTAS)
     cache_attn_kernel(const __grid_constant__ CacheAttnParams p, const __grid_constant__ CUtensorMap tk,
                       const __grid_constant__ CUtensorMap tv) {
   using namespace ptx;

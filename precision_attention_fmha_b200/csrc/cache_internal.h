@@ -48,6 +48,8 @@ struct CacheAttnParams : CacheParams {
 
 // Rows (query token x head of the group) that one CTA takes at once.
 inline int cache_attn_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+// CTAs of an SM: with up to 8 rows three fit its registers.
+constexpr int cache_attn_ctas(int rows) { return rows <= 8 ? 3 : 2; }
 
 cudaError_t launch_cache_attn(int D, bool k8, bool v8, const CacheAttnParams& p, const CUtensorMap& tk,
                               const CUtensorMap& tv, cudaStream_t stream);
