@@ -22,7 +22,11 @@ constexpr int kEvictThreads = 1024, kEvictWarps = kEvictThreads / 32;
 
 // One CTA per (sequence, KV head): the `left`-th largest weight digit by digit
 // (11 + 11 + 10 bits), then the kept positions in ascending order.
+// CACHED: the keys stay in shared memory between the passes.
+constexpr int kEvictCached = 49152;  // keys
+template <bool CACHED>
 __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
+  extern __shared__ uint32_t cached[];
   __shared__ unsigned hist[2048];
   __shared__ unsigned sums[kEvictWarps];
   __shared__ unsigned found[3];  // digit, rank inside it, its size
@@ -46,6 +50,18 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
   }
   const int m0 = p.sinks, m1 = n - p.recent;  // the others: m0 < m1, since sinks + recent <= budget < n
   int left = p.budget - p.sinks - p.recent;
+  if constexpr (CACHED) {
+    for (int i0 = tid; i0 < n; i0 += 8 * kEvictThreads) {
+      float x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = i0 + k * kEvictThreads < n ? __ldg(w + i0 + k * kEvictThreads) : 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (i0 + k * kEvictThreads < n) cached[i0 + k * kEvictThreads] = weight_key(x[k]);
+    }
+    __syncthreads();
+  }
+  auto key_of = [&](int i) { return CACHED ? cached[i] : weight_key(__ldg(w + i)); };
   uint32_t limit = 0xffffffffu;  // keys above it stay, and `left` of those equal to it
   if (left > 0) {
     uint32_t prefix = 0;
@@ -55,7 +71,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
       for (int i = tid; i < 2048; i += kEvictThreads) hist[i] = 0u;
       __syncthreads();
       for (int i = m0 + tid; i < m1; i += kEvictThreads) {
-        const uint32_t k = weight_key(w[i]);
+        const uint32_t k = key_of(i);
         if (pass == 0 || (k >> (shift + bits)) == (prefix >> (shift + bits))) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
       }
       __syncthreads();
@@ -90,7 +106,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
     if (j >= j1) return;
     if (j < m0 || j >= m1) gt = true;
     else {
-      const uint32_t k = weight_key(w[j]);
+      const uint32_t k = key_of(j);
       gt = k > limit;
       eq = k == limit && left > 0;
     }
@@ -161,15 +177,22 @@ __device__ __forceinline__ int kept_count(const CompactParams& p, int b) {
   return n;
 }
 
-// Into another cache: every row on its own. A warp takes 32 rows, K then V,
-// with eight 16-byte loads per lane in flight.
-constexpr int kCopyRows = 32;
+// Into another cache: every row on its own; positions past the kept rows clear
+// their weights. A warp takes 32 rows, one lane looking up each, and moves
+// them with up to eight 16-byte loads per lane in flight: the bytes bound it
+// (537 MB moved in 90 us; 8 rows a warp pay for their lookups, 106 us). With
+// too few rows for that to fill the SMs it takes 8 (4096 rows: 13 -> 7 us).
+__host__ __device__ inline int copy_runs(const CompactParams& p, int rows) {
+  const int n = p.weights_out != nullptr && p.n_weights_out > p.n_keep ? p.n_weights_out : p.n_keep;
+  return (n + rows - 1) / rows;
+}
+template <int kCopyRows>
 __global__ void __launch_bounds__(256) compact_copy_kernel(const __grid_constant__ CompactParams p) {
   const int lane = threadIdx.x & 31;
   long long item = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int h = static_cast<int>(item % p.c.Hkv);
   item /= p.c.Hkv;
-  const int runs = (p.n_keep + kCopyRows - 1) / kCopyRows;
+  const int runs = copy_runs(p, kCopyRows);
   const int run = static_cast<int>(item % runs);
   const int b = static_cast<int>(item / runs);
   if (b >= p.c.B) return;
@@ -179,45 +202,42 @@ __global__ void __launch_bounds__(256) compact_copy_kernel(const __grid_constant
   Place src{0, 0, false}, dst{0, 0, false};
   int from = 0;
   bool ok = false;
-  if (i < count) ok = kept_row(p, b, h, i, start, src, dst, from);
+  if (lane < kCopyRows && i < count) ok = kept_row(p, b, h, i, start, src, dst, from);
   const int64_t ks = src.outer * p.k_sb + src.row * p.k_ss + h * p.k_sh, vs = src.outer * p.v_sb + src.row * p.v_ss + h * p.v_sh;
   const int64_t kd = dst.outer * p.ko_sb + dst.row * p.ko_ss + h * p.ko_sh, vd = dst.outer * p.vo_sb + dst.row * p.vo_ss + h * p.vo_sh;
-  if (p.weights_out != nullptr && ok && start + i < p.n_weights_out) {
+  if (p.weights_out != nullptr && lane < kCopyRows && start + i >= 0 && start + i < p.n_weights_out && (ok || i >= count)) {
     const int64_t bh = static_cast<int64_t>(b) * p.c.Hkv + h;
-    p.weights_out[bh * p.n_weights_out + start + i] = from < p.n_weights ? p.weights[bh * p.n_weights + from] : 0.f;
+    p.weights_out[bh * p.n_weights_out + start + i] = ok && from < p.n_weights ? p.weights[bh * p.n_weights + from] : 0.f;
   }
   const uint32_t live = __ballot_sync(kFull, ok);
   if (live == 0) return;
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int lpr = (t ? p.v_bytes : p.k_bytes) / 16, rpl = 32 / lpr;  // lanes per row; rows per load
-    const int sub = lane / lpr, unit = (lane % lpr) * 16;
-    const uint8_t* from_t = (t ? p.v : p.k) + unit;
-    uint8_t* to_t = (t ? p.v_out : p.k_out) + unit;
-    for (int r0 = 0; r0 < kCopyRows; r0 += 8 * rpl) {
-      uint4 x[8];
+  for (int r0 = 0; r0 < kCopyRows; r0 += 8) {
+    // 8 rows at a time: at most 4 loads of K and 4 of V (256-byte rows, two per warp load).
+    uint4 x[2][4];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int r = r0 + k * rpl + sub;
+    for (int t = 0; t < 2; ++t) {
+      const int lpr = (t ? p.v_bytes : p.k_bytes) / 16, rpl = 32 / lpr;  // lanes per row; rows per load
+      const uint8_t* from_t = (t ? p.v : p.k) + (lane % lpr) * 16;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = r0 + k * rpl + lane / lpr;
         const int64_t at = __shfl_sync(kFull, t ? vs : ks, r & 31);
-        if (r < kCopyRows && ((live >> r) & 1u)) x[k] = __ldg(reinterpret_cast<const uint4*>(from_t + at));
+        if (r < r0 + 8 && ((live >> r) & 1u)) x[t][k] = __ldg(reinterpret_cast<const uint4*>(from_t + at));
       }
+    }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int r = r0 + k * rpl + sub;
+    for (int t = 0; t < 2; ++t) {
+      const int lpr = (t ? p.v_bytes : p.k_bytes) / 16, rpl = 32 / lpr;
+      uint8_t* to_t = (t ? p.v_out : p.k_out) + (lane % lpr) * 16;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = r0 + k * rpl + lane / lpr;
         const int64_t at = __shfl_sync(kFull, t ? vd : kd, r & 31);
-        if (r < kCopyRows && ((live >> r) & 1u)) *reinterpret_cast<uint4*>(to_t + at) = x[k];
+        if (r < r0 + 8 && ((live >> r) & 1u)) *reinterpret_cast<uint4*>(to_t + at) = x[t][k];
       }
     }
   }
-}
-
-// Weights past the kept rows become 0.
-__global__ void __launch_bounds__(256) clear_weights_kernel(const __grid_constant__ CompactParams p) {
-  const int bh = blockIdx.y, b = bh / p.c.Hkv;
-  const int start = (p.dst_start != nullptr ? __ldg(p.dst_start + b) : 0) + kept_count(p, b);
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= max(start, 0) && i < p.n_weights_out) p.weights_out[static_cast<int64_t>(bh) * p.n_weights_out + i] = 0.f;
 }
 
 // Inside one cache: positions never grow (from >= start + i), so rows moved in
@@ -288,7 +308,15 @@ __global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const __grid
 }  // namespace
 
 cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t s) {
-  evict_select_kernel<<<p.c.B * p.c.Hkv, kEvictThreads, 0, s>>>(p);
+  const int n = std::min(p.c.capacity, p.n_weights);
+  if (n <= kEvictCached) {
+    const int smem = std::max(n, 1) * 4;
+    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    evict_select_kernel<true><<<p.c.B * p.c.Hkv, kEvictThreads, smem, s>>>(p);
+  } else {
+    evict_select_kernel<false><<<p.c.B * p.c.Hkv, kEvictThreads, 0, s>>>(p);
+  }
   return cudaGetLastError();
 }
 
@@ -297,11 +325,13 @@ cudaError_t launch_compact(const CompactParams& p, cudaStream_t s) {
     compact_move_kernel<<<dim3(p.c.B * p.c.Hkv, p.k_bytes / 32 + p.v_bytes / 32 + (p.weights_out != nullptr ? 1 : 0)), kMoveThreads, 0, s>>>(p);
     return cudaGetLastError();
   }
-  const long long items = static_cast<long long>(p.c.B) * p.c.Hkv * ((p.n_keep + kCopyRows - 1) / kCopyRows);
-  if (items > 0) compact_copy_kernel<<<static_cast<unsigned>((items + 7) / 8), 256, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || p.weights_out == nullptr || p.n_weights_out == 0) return e;
-  clear_weights_kernel<<<dim3((p.n_weights_out + 255) / 256, p.c.B * p.c.Hkv), 256, 0, s>>>(p);
+  const long long heads = static_cast<long long>(p.c.B) * p.c.Hkv;
+  const bool wide = heads * copy_runs(p, 32) >= 4096;  // warps: about 28 per SM
+  const long long items = heads * copy_runs(p, wide ? 32 : 8);
+  if (items == 0) return cudaSuccess;
+  const unsigned grid = static_cast<unsigned>((items + 7) / 8);
+  if (wide) compact_copy_kernel<32><<<grid, 256, 0, s>>>(p);
+  else compact_copy_kernel<8><<<grid, 256, 0, s>>>(p);
   return cudaGetLastError();
 }
 

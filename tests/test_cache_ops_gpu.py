@@ -83,6 +83,28 @@ def test_pick_ties_go_to_the_lowest_block():
     assert got.flatten().tolist() == [0, 1, 2, 3]
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_pick_near_ties(D):
+    """Scores that differ by less than 32 bits can tell (many blocks within 2^-24 of each other): the exact ones decide."""
+    from precision_attention_fmha_b200 import fmha
+
+    g = torch.Generator(device=DEV)
+    g.manual_seed(D)
+    n = 1000
+    q = torch.randn(2, 2, 6, D, generator=g, device=DEV).bfloat16()
+    one = torch.randn(2, 3, 1, 2, D, generator=g, device=DEV)
+    one = torch.stack([one.amin(3), one.amax(3)], 3).bfloat16().expand(2, 3, n, 2, D).contiguous()
+    # one channel moves by a tiny amount: products of 2^-20 and less next to a score of order 10
+    one[..., 0, 3] = -(torch.randint(1, 100, (2, 3, n), generator=g, device=DEV) * 2.0 ** -27).bfloat16()
+    one[..., 1, 3] = (torch.randint(1, 100, (2, 3, n), generator=g, device=DEV) * 2.0 ** -27).bfloat16()
+    lens = [n * 16, n * 16 - 40]
+    got = fmha.select_blocks(q, one, i32(lens), 16, 300, 1, 2)
+    for b, rows in enumerate(ref.pick(q, one, lens, 16, 300, 1, 2)):
+        for t, heads in enumerate(rows):
+            for h, ids in enumerate(heads):
+                assert got[b, t, h].tolist() == ids
+
+
 @pytest.mark.parametrize("B,T,Hq,Hkv,D,lens,top,sinks,recent", [
     (1, 128, 2, 1, 64, [128], 1, 0, 1), (1, 700, 8, 2, 128, [700], 3, 1, 1), (2, 300, 4, 4, 128, [300, 900], 2, 0, 1),
     (2, 513, 4, 1, 64, [513, 200], 4, 1, 2),
