@@ -444,9 +444,13 @@ fmha_status fmha_select_blocks(const fmha_cache_args* args, const void* bounds, 
  *   Reads q, k, lse, lens, q_lens and sf_k of args.
  *   weights: fp32 [B, Hkv, n_weights] contiguous, device; accumulate != 0 adds,
  *     0 overwrites. Entries at or past lens[b] are left as they were;
- *     lens[b] <= n_weights. The same inputs give the same bits.             */
+ *     lens[b] <= n_weights. The same inputs give the same bits.
+ *   workspace: device, 16-byte aligned, caller-owned, at least
+ *     fmha_key_weights_workspace_bytes(args, n_weights, causal) bytes (0, and
+ *     NULL, for a few query tokens); not shared with a call that may overlap. */
 fmha_status fmha_key_weights(const fmha_cache_args* args, float* weights, int32_t n_weights, int32_t causal,
-                             int32_t accumulate, struct CUstream_st* stream);
+                             int32_t accumulate, void* workspace, size_t workspace_bytes, struct CUstream_st* stream);
+size_t fmha_key_weights_workspace_bytes(const fmha_cache_args* args, int32_t n_weights, int32_t causal);
 
 /* The keys of each (sequence, KV head) that stay under a budget. With
  * n = lens[b] > budget: the first `sinks`, the last `recent`, and of the others

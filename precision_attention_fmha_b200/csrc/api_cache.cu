@@ -204,6 +204,20 @@ constexpr int kMaxPickBlocks = 16384;  // their 64-bit scores fit one CTA's shar
 // Query tokens from which fmha_key_weights runs on the tensor cores' 128-token tiles.
 constexpr int kManyQueries = 64;
 
+// How a prompt's query tiles (128 tokens of one head) are cut into runs: about four per resident CTA in all, so that
+// the last ones to end differ little, each of at least 8 tiles (its keys are loaded anew).
+struct WeightRuns {
+  int chunk, parts;
+};
+WeightRuns weight_runs(const fmha_cache_args* a, int capacity, int n_weights, int causal) {
+  const int64_t most = static_cast<int64_t>(ceil_div(a->T, 128)) * (a->Hq / a->Hkv);  // of one key tile
+  const int64_t keys = ceil_div(std::min(capacity, n_weights), 128);
+  int64_t total = static_cast<int64_t>(a->B) * a->Hkv * keys * most;
+  if (causal && capacity <= 2 * static_cast<int64_t>(a->T)) total /= 2;
+  const int64_t chunk = std::min(most, std::max<int64_t>(8, total / (8 * sm_count())));
+  return {static_cast<int>(chunk), static_cast<int>((most + chunk - 1) / chunk)};
+}
+
 // CTAs that score the blocks of one item: up to three per SM, while each keeps at least the 32 blocks that its warps
 // load at once (items 256, 512 blocks: one CTA each 34 us, two 22 us).
 int pick_cluster(int64_t items, int n_blocks) {
@@ -461,8 +475,14 @@ fmha_status fmha_select_blocks(const fmha_cache_args* a, const void* bounds, int
   return ok_status();
 }
 
+size_t fmha_key_weights_workspace_bytes(const fmha_cache_args* a, int32_t n_weights, int32_t causal) {
+  if (!rows_ok(a) || n_weights <= 0 || capacity_of(a) <= 0 || capacity_of(a) > INT32_MAX / 2 || a->T < kManyQueries) return 0;
+  const WeightRuns r = weight_runs(a, static_cast<int>(capacity_of(a)), n_weights, causal);
+  return r.parts > 1 ? size_t(r.parts) * a->B * a->Hkv * n_weights * 4 : 0;
+}
+
 fmha_status fmha_key_weights(const fmha_cache_args* a, float* weights, int32_t n_weights, int32_t causal,
-                             int32_t accumulate, cudaStream_t stream) {
+                             int32_t accumulate, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   if (a == nullptr) return fail(FMHA_ERR_INVALID_ARG, "args is NULL");
   if (!sizes_ok(a) || n_weights < 0) return fail(FMHA_ERR_INVALID_ARG, "negative size");
   if (a->B == 0 || a->T == 0 || a->Hq == 0 || n_weights == 0) return ok_status();
@@ -491,9 +511,16 @@ fmha_status fmha_key_weights(const fmha_cache_args* a, float* weights, int32_t n
   cudaError_t e;
   CUtensorMap m;
   if (a->T >= kManyQueries) {
-    const int64_t n = heads * ceil_div(std::min(p.c.capacity, n_weights), 128);
-    if (n >= (int64_t(1) << 31)) return fail(FMHA_ERR_UNSUPPORTED, "grid too large");
+    const WeightRuns r = weight_runs(a, p.c.capacity, n_weights, causal);
+    const int64_t n = heads * ceil_div(std::min(p.c.capacity, n_weights), 128) * r.parts;
+    if (n >= (int64_t(1) << 31) || heads > 65535) return fail(FMHA_ERR_UNSUPPORTED, "grid too large");
     p.n_ctas = static_cast<int>(n);
+    p.chunk = r.chunk;
+    p.parts = r.parts;
+    if (r.parts > 1) {
+      if ((st = check_workspace(workspace, workspace_bytes, size_t(r.parts) * heads * n_weights * 4)) != FMHA_OK) return st;
+      p.part_w = static_cast<float*>(workspace);
+    }
     const uint64_t dims[4] = {uint64_t(a->D), uint64_t(a->Hq), uint64_t(a->T), uint64_t(a->B)};
     const int64_t strides[3] = {a->q.stride_h, a->q.stride_s, a->q.stride_b};
     const uint32_t box[4] = {64, 1, 128, 1};

@@ -63,6 +63,9 @@ struct KeyWeightsParams : CacheParams {
   const float* lse;  // [B, Hq, T]
   float* weights;    // [B, Hkv, n_weights]
   int32_t n_weights, causal, accumulate;
+  // prompts: query tiles of one CTA, the most runs of them a key tile has, and (several runs) their sums
+  int32_t chunk, parts;
+  float* part_w;     // [parts, B, Hkv, n_weights]
   float scale_log2;
   const float* sf_k; int32_t sf_k_kind;
 };

@@ -94,10 +94,11 @@ def load_library(path=None):
     lib.fmha_fwd_selected_workspace_bytes.argtypes = [cache, i32, i32]
     lib.fmha_key_bounds.argtypes = [cache, vp, i32, i32, vp, vp]
     lib.fmha_select_blocks.argtypes = [cache, vp, i32, i32, i32, i32, i32, i32, vp, vp]
-    lib.fmha_key_weights.argtypes = [cache, vp, i32, i32, i32, vp]
+    lib.fmha_key_weights.argtypes = [cache, vp, i32, i32, i32, vp, sz, vp]
+    lib.fmha_key_weights_workspace_bytes.argtypes = [cache, i32, i32]
     lib.fmha_evict_select.argtypes = [cache, vp, i32, i32, i32, i32, vp, vp, vp]
     lib.fmha_cache_compact.argtypes = [cache, cache, vp, i64, i64, i32, vp, vp, vp, i32, vp, i32, vp]
-    for f in ("fmha_fwd_tree_workspace_bytes", "fmha_fwd_selected_workspace_bytes"):
+    for f in ("fmha_fwd_tree_workspace_bytes", "fmha_fwd_selected_workspace_bytes", "fmha_key_weights_workspace_bytes"):
         getattr(lib, f).restype = sz
     lib.fmha_status_string.argtypes = [ctypes.c_int]
     lib.fmha_status_string.restype = ctypes.c_char_p
@@ -639,7 +640,7 @@ def select_blocks(q, bounds, lens, block, top, sink_blocks=0, recent_blocks=1, q
 
 
 def key_weights(q, k, lse, weights, lens, q_lens=None, page_table=None, causal=True, accumulate=True,
-                sf_k=None, softmax_scale=None, stream=None):
+                sf_k=None, softmax_scale=None, workspace=None, stream=None):
     """Adds (accumulate=False: writes) to weights fp32 [B, Hkv, n] the attention weight each key gathers over q.
 
     weights[b, h, s] (+)= sum_t sum_g exp(scale * q_tg . k_s - lse[b, g, t]), over the query heads g of KV head h
@@ -651,7 +652,9 @@ def key_weights(q, k, lse, weights, lens, q_lens=None, page_table=None, causal=T
     w = _floats(weights, (B, Hkv, weights.shape[2]), "weights")
     lib = load_library()
     with _launch(stream, q, k, lse, weights, lens, q_lens, page_table, *_sf_tensors(sf_k)) as s:
-        _check(lib.fmha_key_weights(a, w, weights.shape[2], 1 if causal else 0, 1 if accumulate else 0, s))
+        n, causal = weights.shape[2], 1 if causal else 0
+        workspace, ptr, size = _scratch(workspace, lib.fmha_key_weights_workspace_bytes(a, n, causal), q)
+        _check(lib.fmha_key_weights(a, w, n, causal, 1 if accumulate else 0, ptr, size, s))
     return weights
 
 
