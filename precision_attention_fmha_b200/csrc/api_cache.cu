@@ -107,7 +107,7 @@ fmha_status cache_map(CUtensorMap* m, const fmha_cache_args* a, const CacheView&
 
 constexpr int kPackedRows = 64;       // packed rows (T * G), and
 constexpr int kPackedKeys = 1024;     // keys of room, from which the context goes to the packed kernel
-constexpr int kPackedCtasPerSm = 3;
+constexpr int kPackedCtasPerSm = 2;
 
 // The sizes of an attention call that do not need the device: grid and row
 // tiles of the tree form.
@@ -214,8 +214,13 @@ WeightRuns weight_runs(const fmha_cache_args* a, int capacity, int n_weights, in
   const int64_t keys = ceil_div(std::min(capacity, n_weights), 128);
   int64_t total = static_cast<int64_t>(a->B) * a->Hkv * keys * most;
   if (causal && capacity <= 2 * static_cast<int64_t>(a->T)) total /= 2;
-  const int64_t chunk = std::min(most, std::max<int64_t>(8, total / (8 * sm_count())));
+  const int64_t chunk = std::min(most, std::max<int64_t>(8, total / (16 * sm_count())));
   return {static_cast<int>(chunk), static_cast<int>((most + chunk - 1) / chunk)};
+}
+
+// The item counter, then (several runs) their sums.
+size_t weight_bytes(const fmha_cache_args* a, const WeightRuns& r, int n_weights) {
+  return 16 + (r.parts > 1 ? size_t(r.parts) * a->B * a->Hkv * n_weights * 4 : 0);
 }
 
 // CTAs that score the blocks of one item: up to three per SM, while each keeps at least the 32 blocks that its warps
@@ -478,7 +483,7 @@ fmha_status fmha_select_blocks(const fmha_cache_args* a, const void* bounds, int
 size_t fmha_key_weights_workspace_bytes(const fmha_cache_args* a, int32_t n_weights, int32_t causal) {
   if (!rows_ok(a) || n_weights <= 0 || capacity_of(a) <= 0 || capacity_of(a) > INT32_MAX / 2 || a->T < kManyQueries) return 0;
   const WeightRuns r = weight_runs(a, static_cast<int>(capacity_of(a)), n_weights, causal);
-  return r.parts > 1 ? size_t(r.parts) * a->B * a->Hkv * n_weights * 4 : 0;
+  return weight_bytes(a, r, n_weights);
 }
 
 fmha_status fmha_key_weights(const fmha_cache_args* a, float* weights, int32_t n_weights, int32_t causal,
@@ -514,13 +519,13 @@ fmha_status fmha_key_weights(const fmha_cache_args* a, float* weights, int32_t n
     const WeightRuns r = weight_runs(a, p.c.capacity, n_weights, causal);
     const int64_t n = heads * ceil_div(std::min(p.c.capacity, n_weights), 128) * r.parts;
     if (n >= (int64_t(1) << 31) || heads > 65535) return fail(FMHA_ERR_UNSUPPORTED, "grid too large");
-    p.n_ctas = static_cast<int>(n);
+    if ((st = check_workspace(workspace, workspace_bytes, weight_bytes(a, r, n_weights))) != FMHA_OK) return st;
+    p.n_ctas = static_cast<int>(std::min<int64_t>(n, 2 * sm_count()));
+    p.n_items = static_cast<uint32_t>(n);
     p.chunk = r.chunk;
     p.parts = r.parts;
-    if (r.parts > 1) {
-      if ((st = check_workspace(workspace, workspace_bytes, size_t(r.parts) * heads * n_weights * 4)) != FMHA_OK) return st;
-      p.part_w = static_cast<float*>(workspace);
-    }
+    p.ticket = static_cast<uint32_t*>(workspace);
+    p.part_w = static_cast<float*>(workspace) + 4;
     const uint64_t dims[4] = {uint64_t(a->D), uint64_t(a->Hq), uint64_t(a->T), uint64_t(a->B)};
     const int64_t strides[3] = {a->q.stride_h, a->q.stride_s, a->q.stride_b};
     const uint32_t box[4] = {64, 1, 128, 1};

@@ -66,6 +66,8 @@ struct KeyWeightsParams : CacheParams {
   // prompts: query tiles of one CTA, the most runs of them a key tile has, and (several runs) their sums
   int32_t chunk, parts;
   float* part_w;     // [parts, B, Hkv, n_weights]
+  uint32_t* ticket;  // next item (key tile, run)
+  uint32_t n_items;
   float scale_log2;
   const float* sf_k; int32_t sf_k_kind;
 };

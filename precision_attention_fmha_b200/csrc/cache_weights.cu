@@ -155,47 +155,28 @@ __global__ void __launch_bounds__(C::THREADS, 2)
   __syncthreads();
 }
 
-// 2^x on the FMA pipe, two values at once, for the share of the exponentials
-// that the special-function pipe (4 a cycle and scheduler, against 2 x 16 FMAs)
-// would otherwise bound: x = n + f, n = rint(x) by adding 1.5 * 2^23, f in
-// [-1/2, 1/2], 2^f by a polynomial of degree 5 fitted to the least relative
-// error there (Remez exchange; 2.1e-7 in 32 bits), and n added to the exponent
-// bits. x is cut at -126: 2^-126 then stands for anything smaller.
-__device__ __forceinline__ void exp2_fma2(float& a, float& b) {
-  using namespace ptx;
-  a = fmaxf(a, -126.f);
-  b = fmaxf(b, -126.f);
-  float ja, jb, fa, fb, pa, pb;
-  fadd2(ja, jb, a, b, 12582912.f, 12582912.f);
-  fadd2(fa, fb, ja, jb, -12582912.f, -12582912.f);
-  fadd2(fa, fb, a, b, -fa, -fb);
-  ffma2(pa, pb, fa, fb, 0.0013276472454890609f, 0.0013276472454890609f, 0.009675540961325169f, 0.009675540961325169f);
-  ffma2(pa, pb, pa, pb, fa, fb, 0.05550713092088699f, 0.05550713092088699f);
-  ffma2(pa, pb, pa, pb, fa, fb, 0.24022120237350464f, 0.24022120237350464f);
-  ffma2(pa, pb, pa, pb, fa, fb, 0.6931469440460205f, 0.6931469440460205f);
-  ffma2(pa, pb, pa, pb, fa, fb, 1.0000001192092896f, 1.0000001192092896f);
-  a = __int_as_float(__float_as_int(pa) + (__float_as_int(ja) << 23));
-  b = __int_as_float(__float_as_int(pb) + (__float_as_int(jb) << 23));
-}
-
 // ---- prompts: S^T = K Q^T on the tensor cores ----
-// A CTA owns 128 keys (TMEM lanes) and streams the query tiles (128 tokens of
+// A CTA takes 128 keys (TMEM lanes) and streams the query tiles (128 tokens of
 // one head, TMEM columns) that see them: with the keys along the lanes the sum
 // over queries is a sum over a thread's own columns, and no value crosses
-// threads. Per tile: 4 D / 64 tensor instructions, then 128 x 128 exponentials.
+// threads. Per tile: 4 D / 64 tensor instructions, then 128 x 128 exponentials
+// by two warpgroups, 64 columns each (one warpgroup, two warps a scheduler,
+// was bound by its latencies: 290 us for 6144 tokens, the pipes half idle).
 // The first keys of a causal prompt are seen by all queries and the last by
-// few, so a key tile's queries are cut into runs of p.chunk tiles that go to
-// CTAs of their own; a run's sums go to the workspace and are added in order.
-// kPolyOf8 of every 8 groups of exponentials go through the FMA pipe.
-constexpr int kPolyOf8 = 3;
+// few, so a key tile's queries are cut into runs of p.chunk tiles; two CTAs
+// per SM draw (key tile, run) items from a counter, the largest first, and a
+// run's sums go to the workspace, where they are added in order.
+// (A share of the exponentials as polynomials on the FMA pipe made it slower:
+// 280 us without, 285 with a quarter, 312 with half: issue slots bound it.)
 template <int D_>
 struct KmCfg {
   static constexpr int D = D_;
   static constexpr int CHUNKS = D / 64;          // 128-byte swizzle columns
   static constexpr int TILE = CHUNKS * 16384;    // 128 rows
   static constexpr int STAGES = 2;
-  static constexpr int SMEM = 1024 + (1 + STAGES) * TILE + 4608;
-  static constexpr int THREADS = 192;
+  static constexpr int SMEM = 1024 + (1 + STAGES) * TILE + 6144;
+  static constexpr int SUM_THREADS = 256, THREADS = 320;
+  static constexpr int MMA_WARP = 8, LOAD_WARP = 9;
   static constexpr uint32_t TMEM_COLS = 256;     // two score buffers
   static constexpr uint32_t IDESC = ptx::make_idesc(1, 1, 1, 0, 0, 128, 128);
 };
@@ -203,49 +184,47 @@ struct alignas(16) KmMisc {
   uint64_t q_full[2], q_empty[2], s_full[2], s_free[2], nl_full[8], drain;
   uint32_t tmem_base;
   volatile uint32_t abort;
+  uint32_t item[2];
+  uint32_t pad[2];
   // -lse of a query tile's tokens, log2 units. Written by the query producer at
   // most 2 tiles ahead of the products, which run at most 2 ahead of a warp's
   // sums: with 8 slots, and a barrier each, neither a slot nor its barrier's
   // phase can come round again before every warp has used it.
   float nl[8][128];
+  double half[128];  // the second warpgroup's sums
 };
-static_assert(sizeof(KmMisc) <= 4608, "misc area");
+static_assert(sizeof(KmMisc) <= 6144, "misc area");
 
-// A thread's sum over the 128 tokens of one score tile (columns tS ..): its key
+// A thread's sum over 64 tokens of one score tile (columns tS ..): its key
 // against tokens t0 .., of which (EDGE) those from `first` on, in use, count.
 template <bool EDGE>
-__device__ __forceinline__ float weigh_tile(const KeyWeightsParams& p, const SeqLens s, uint32_t tS, const float4* nl,
-                                            float c, uint32_t s_free, int t0, int first) {
+__device__ __forceinline__ float weigh_tile(const SeqLens s, uint32_t tS, const float4* nl, float c, uint32_t s_free,
+                                            int t0, int first) {
   using namespace ptx;
   float r0 = 0.f, r1 = 0.f, r2 = 0.f, r3 = 0.f;
 #pragma unroll
   for (int ch = 0; ch < 2; ++ch) {
-    uint32_t x[2][32];
-    tmem_ld32(tS + 64 * ch, x[0]);
-    tmem_ld32(tS + 64 * ch + 32, x[1]);
+    uint32_t x[32];
+    tmem_ld32(tS + 32 * ch, x);
     tmem_wait_ld();
-    reg_fence(x[0]);
-    reg_fence(x[1]);
+    reg_fence(x);
     if (ch == 1) {  // the scores are in registers: the next product may overwrite them
       tc_fence_before();
       __syncwarp();
       if ((threadIdx.x & 31) == 0) mbar_arrive(s_free);
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float4 n = nl[16 * ch + i];
+    for (int i = 0; i < 8; ++i) {
+      const float4 n = nl[8 * ch + i];
       float e0, e1, e2, e3;
-      const uint32_t* y = &x[i >> 3][4 * (i & 7)];
-      ffma2(e0, e1, __uint_as_float(y[0]), __uint_as_float(y[1]), c, c, n.x, n.y);
-      ffma2(e2, e3, __uint_as_float(y[2]), __uint_as_float(y[3]), c, c, n.z, n.w);
-      if ((i * kPolyOf8) % 8 < kPolyOf8) {
-        exp2_fma2(e0, e1);
-        exp2_fma2(e2, e3);
-      } else {
-        e0 = ex2(e0); e1 = ex2(e1); e2 = ex2(e2); e3 = ex2(e3);
-      }
+      const uint32_t* y = &x[4 * i];
+      e0 = fmaf(__uint_as_float(y[0]), c, n.x);
+      e1 = fmaf(__uint_as_float(y[1]), c, n.y);
+      e2 = fmaf(__uint_as_float(y[2]), c, n.z);
+      e3 = fmaf(__uint_as_float(y[3]), c, n.w);
+      e0 = ex2(e0); e1 = ex2(e1); e2 = ex2(e2); e3 = ex2(e3);
       if constexpr (EDGE) {
-        const int t = t0 + 64 * ch + 4 * i;
+        const int t = t0 + 32 * ch + 4 * i;
         e0 = t < s.q && t >= first ? e0 : 0.f;
         e1 = t + 1 < s.q && t + 1 >= first ? e1 : 0.f;
         e2 = t + 2 < s.q && t + 2 >= first ? e2 : 0.f;
@@ -268,76 +247,92 @@ __global__ void __launch_bounds__(KmCfg<D>::THREADS, 2)
   uint8_t* sQ = sK + C::TILE;
   KmMisc* misc = reinterpret_cast<KmMisc*>(sQ + C::STAGES * C::TILE);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // Key tiles in order: the first are seen by the most queries and start first.
   const int bh_n = p.c.B * p.c.Hkv;
-  const int part = blockIdx.x % p.parts, tile = blockIdx.x / p.parts;
-  const int kt = tile / bh_n, bh = tile - kt * bh_n;
-  const int b = bh / p.c.Hkv, hkv = bh - b * p.c.Hkv;
-  bool bad;
-  const SeqLens s = seq_lens(p.c, b, bad);
-  if (kt == 0 && hkv == 0 && part == 0 && tid == 0 && (bad || s.len > p.n_weights)) atomicOr(p.c.err, kErrLength);
-  const int key0 = kt * 128;
-  const int n_keys = min(128, min(s.len, p.n_weights) - key0);
-  if (n_keys <= 0) return;
-  const int base = s.len - s.q;  // position of token 0
-  const int tt0 = p.causal ? max(0, key0 - base) / 128 : 0;
-  const int n_tt = max(0, (s.q + 127) / 128 - tt0);
-  const int it0 = part * p.chunk;  // this run's tiles: it0 + [0, n_it) of n_tt * G
-  const int n_it = min(p.chunk, n_tt * p.c.G - it0);
-  if (n_it <= 0 && part > 0) return;
-
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&misc->q_full[i]), 1);
       mbar_init(smem_addr(&misc->q_empty[i]), 1);
       mbar_init(smem_addr(&misc->s_full[i]), 1);
-      mbar_init(smem_addr(&misc->s_free[i]), 4);
+      mbar_init(smem_addr(&misc->s_free[i]), C::SUM_THREADS / 32);
     }
     for (int i = 0; i < 8; ++i) mbar_init(smem_addr(&misc->nl_full[i]), 32);
     mbar_init(smem_addr(&misc->drain), 1);
     misc->abort = 0u;
+    misc->item[0] = atomicAdd(p.ticket, 1u);
     fence_barrier_init();
   }
-  if (warp == 4) {
+  if (warp == C::MMA_WARP) {
     tmem_alloc(smem_addr(&misc->tmem_base), C::TMEM_COLS);
     tmem_relinquish();
   }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc->tmem_base;
   const Waiter w{&misc->abort, p.c.err, p.c.wait_cycles};
-  // Query tile `it`: the copy, and the log-sum-exps of its 128 tokens (four per lane, one tile ahead in registers).
-  float lse4[4];
-  auto fetch_lse = [&](int it) {
-    const int t = (tt0 + (it0 + it) / p.c.G) * 128 + 4 * lane, head = hkv * p.c.G + (it0 + it) % p.c.G;
+  const bool leader = warp == C::MMA_WARP && elect_one();
+  int cnt = 0;     // tiles of the items before this one: slots and phases run on
+  int copies = 0;  // load warp: query tiles sent
+
+  for (int turn = 0;; ++turn) {
+    // Items in order: the first keys are seen by the most queries and start first.
+    const uint32_t item = misc->item[turn & 1];
+    if (item >= p.n_items || misc->abort) break;
+    const int part = item % p.parts, tile = item / p.parts;
+    const int kt = tile / bh_n, bh = tile - kt * bh_n;
+    const int b = bh / p.c.Hkv, hkv = bh - b * p.c.Hkv;
+    if (warp == C::LOAD_WARP && lane == 0) misc->item[(turn + 1) & 1] = atomicAdd(p.ticket, 1u);
+    bool bad;
+    const SeqLens s = seq_lens(p.c, b, bad);
+    if (kt == 0 && hkv == 0 && part == 0 && tid == 0 && (bad || s.len > p.n_weights)) atomicOr(p.c.err, kErrLength);
+    const int key0 = kt * 128;
+    const int n_keys = min(128, min(s.len, p.n_weights) - key0);
+    const int base = s.len - s.q;  // position of token 0
+    const int tt0 = p.causal ? max(0, key0 - base) / 128 : 0;
+    const int n_tt = max(0, (s.q + 127) / 128 - tt0);
+    const int it0 = part * p.chunk;  // this run's tiles: it0 + [0, n_it) of n_tt * G
+    const int n_it = min(p.chunk, n_tt * p.c.G - it0);
+    if (n_keys <= 0 || (n_it <= 0 && part > 0)) {
+      __syncthreads();  // the next item is there
+      continue;
+    }
+    // Query tile `it`: the copy, and the log-sum-exps of its 128 tokens (four per lane, one tile ahead in registers).
+    float lse4[4];
+    auto fetch_lse = [&](int it) {
+      const int t = (tt0 + (it0 + it) / p.c.G) * 128 + 4 * lane, head = hkv * p.c.G + (it0 + it) % p.c.G;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      lse4[e] = it < n_it && t + e < s.q ? neg_lse2(__ldg(p.lse + (static_cast<int64_t>(b) * p.c.Hq + head) * p.c.T + t + e)) : -INFINITY;
-  };
-  auto send_query = [&](int it) {
-    const int st = it & 1;
-    const uint32_t full = smem_addr(&misc->q_full[st]);
-    if (lane == 0) mbar_arrive_expect_tx(full, C::TILE);
-    __syncwarp();
-    const int tt = tt0 + (it0 + it) / p.c.G, head = hkv * p.c.G + (it0 + it) % p.c.G;
-    if (lane < C::CHUNKS) tma_load_4d(smem_addr(sQ + st * C::TILE) + lane * 16384, &tq, full, lane * 64, head, tt * 128, b);
-    *reinterpret_cast<float4*>(&misc->nl[it & 7][4 * lane]) = make_float4(lse4[0], lse4[1], lse4[2], lse4[3]);
-    mbar_arrive(smem_addr(&misc->nl_full[it & 7]));
-    fetch_lse(it + 1);
-  };
-  int sent = 0;
-  if (warp == 5) {  // the first two tiles load while the keys do
-    fetch_lse(0);
-    for (; sent < min(2, n_it); ++sent) send_query(sent);
-  } else {
-    // The keys, as BF16 rows in the 128-byte swizzle (E4M3 codes are BF16 values; the scale joins the score): eight
-    // 16-byte units per thread in flight.
-    constexpr int UNITS = 128 * (D / 8), STEP = 160;
-    for (int i0 = tid; i0 < UNITS; i0 += 8 * STEP) {
-      uint4 v[8];
+      for (int e = 0; e < 4; ++e)
+        lse4[e] = it < n_it && t + e < s.q ? neg_lse2(__ldg(p.lse + (static_cast<int64_t>(b) * p.c.Hq + head) * p.c.T + t + e)) : -INFINITY;
+    };
+    auto send_query = [&](int it) -> bool {
+      const int n = cnt + it, st = n & 1;
+      if (!__all_sync(kFull, w.wait(smem_addr(&misc->q_empty[st]), ((n >> 1) & 1) ^ 1))) return false;
+      const uint32_t full = smem_addr(&misc->q_full[st]);
+      if (lane == 0) mbar_arrive_expect_tx(full, C::TILE);
+      __syncwarp();
+      const int tt = tt0 + (it0 + it) / p.c.G, head = hkv * p.c.G + (it0 + it) % p.c.G;
+      if (lane < C::CHUNKS) tma_load_4d(smem_addr(sQ + st * C::TILE) + lane * 16384, &tq, full, lane * 64, head, tt * 128, b);
+      *reinterpret_cast<float4*>(&misc->nl[n & 7][4 * lane]) = make_float4(lse4[0], lse4[1], lse4[2], lse4[3]);
+      mbar_arrive(smem_addr(&misc->nl_full[n & 7]));
+      ++copies;
+      fetch_lse(it + 1);
+      return true;
+    };
+    int sent = 0;
+    bool ok = true;
+    if (warp == C::LOAD_WARP) {  // the first two tiles load while the keys do
+      fetch_lse(0);
+      for (; sent < min(2, n_it) && ok; sent += ok) ok = send_query(sent);
+    } else if (warp < C::MMA_WARP) {
+      // The keys, as BF16 rows in the 128-byte swizzle (E4M3 codes are BF16 values; the scale joins the score): all of a
+      // thread's 16-byte units in flight at once.
+      constexpr int N = 128 * (D / 8) / C::SUM_THREADS;
+      uint4 v[N];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int i = i0 + k * STEP, r = i / (D / 8), u = i % (D / 8);
+      for (int k = 0; k < N; ++k) {
+        const int i = tid + k * C::SUM_THREADS, r = i / (D / 8), u = i % (D / 8);
         v[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (i < UNITS && r < n_keys) {
+        if (r < n_keys) {
           const Piece e = cache_piece(p.c, b, key0 + r, s.len);
           if (p.c.page_table == nullptr || e.outer < p.c.num_pages) {  // a bad page reads zeros
             const int64_t at = e.outer * p.k_sb + e.row * p.k_ss + hkv * p.k_sh + u * 8;
@@ -352,89 +347,84 @@ __global__ void __launch_bounds__(KmCfg<D>::THREADS, 2)
         }
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int i = i0 + k * STEP, r = i / (D / 8), u = i % (D / 8);
+      for (int k = 0; k < N; ++k) {
+        const int i = tid + k * C::SUM_THREADS, r = i / (D / 8), u = i % (D / 8);
         if constexpr (K8)
           v[k] = make_uint4(e4m3x2_to_bf16x2(v[k].x & 0xffffu), e4m3x2_to_bf16x2(v[k].x >> 16),
                             e4m3x2_to_bf16x2(v[k].y & 0xffffu), e4m3x2_to_bf16x2(v[k].y >> 16));
-        if (i < UNITS) *reinterpret_cast<uint4*>(sK + (u >> 3) * 16384 + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = v[k];
+        *reinterpret_cast<uint4*>(sK + (u >> 3) * 16384 + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = v[k];
       }
+      fence_proxy_async_smem();  // the tensor cores read them
     }
-  }
-  fence_proxy_async_smem();  // the tensor cores read them
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = misc->tmem_base;
+    __syncthreads();
 
-  if (warp == 5) {  // query tiles
-    bool ok = true;
-    for (; sent < n_it; ++sent) {
-      ok = __all_sync(kFull, w.wait(smem_addr(&misc->q_empty[sent & 1]), ((sent >> 1) & 1) ^ 1));
-      if (!ok) break;
-      send_query(sent);
-    }
-    if (lane == 0)
-      for (int k = sent > 2 ? sent - 2 : 0; k < sent; ++k) w.drain(smem_addr(&misc->q_full[k & 1]), (k >> 1) & 1);
-    __syncwarp();
-  } else if (warp == 4) {  // S^T = K Q^T
-    const bool leader = elect_one();
-    auto lo = [](uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | (1u << 16); };
-    const uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
-    const uint32_t k_lo = lo(smem_addr(sK)), q_lo = lo(smem_addr(sQ));
-    bool ok = true;
-    for (int it = 0; it < n_it && ok; ++it) {
-      const int st = it & 1;
-      const uint32_t ph = (it >> 1) & 1;
-      ok = __all_sync(kFull, w.wait(smem_addr(&misc->q_full[st]), ph)) &&
-           __all_sync(kFull, w.wait(smem_addr(&misc->s_free[st]), ph ^ 1));
-      if (!ok) break;
-      tc_fence_after();
-      if (leader) {
+    if (warp == C::LOAD_WARP) {  // query tiles
+      for (; sent < n_it && ok; sent += ok) ok = send_query(sent);
+    } else if (warp == C::MMA_WARP) {  // S^T = K Q^T
+      auto lo = [](uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | (1u << 16); };
+      const uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
+      const uint32_t k_lo = lo(smem_addr(sK)), q_lo = lo(smem_addr(sQ));
+      for (int it = 0; it < n_it; ++it) {
+        const int n = cnt + it, st = n & 1;
+        const uint32_t ph = (n >> 1) & 1;
+        if (!__all_sync(kFull, w.wait(smem_addr(&misc->q_full[st]), ph)) ||
+            !__all_sync(kFull, w.wait(smem_addr(&misc->s_free[st]), ph ^ 1)))
+          break;
+        tc_fence_after();
+        if (leader) {
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint32_t off = ((i / 4) * 16384 + (i % 4) * 32) >> 4;
-          const uint32_t q = q_lo + st * (C::TILE >> 4) + off;
-          if (i == 0) mma_ss_f16_lean<false>(tmem + st * 128, k_lo + off, hi, q, hi, C::IDESC);
-          else mma_ss_f16_lean<true>(tmem + st * 128, k_lo + off, hi, q, hi, C::IDESC);
+          for (int i = 0; i < D / 16; ++i) {
+            const uint32_t off = ((i / 4) * 16384 + (i % 4) * 32) >> 4;
+            const uint32_t q = q_lo + st * (C::TILE >> 4) + off;
+            if (i == 0) mma_ss_f16_lean<false>(tmem + st * 128, k_lo + off, hi, q, hi, C::IDESC);
+            else mma_ss_f16_lean<true>(tmem + st * 128, k_lo + off, hi, q, hi, C::IDESC);
+          }
+          tc_commit(smem_addr(&misc->s_full[st]));
+          tc_commit(smem_addr(&misc->q_empty[st]));
         }
-        tc_commit(smem_addr(&misc->s_full[st]));
-        tc_commit(smem_addr(&misc->q_empty[st]));
+        __syncwarp();
       }
-      __syncwarp();
+    } else {  // one key per thread, 64 tokens of each tile
+      const int row = tid & 127, side = tid >> 7, key = key0 + row;
+      const float c = p.scale_log2 * sf_of(p.sf_k, p.sf_k_kind, bh);
+      const uint32_t tS = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + side * 64;
+      double total = 0.0;  // 32 bits inside a tile, 64 across: a prompt's sum has tens of thousands of terms
+      for (int it = 0; it < n_it; ++it) {
+        const int n = cnt + it, st = n & 1;
+        ok = __all_sync(kFull, w.wait(smem_addr(&misc->s_full[st]), (n >> 1) & 1)) &&
+             __all_sync(kFull, w.wait(smem_addr(&misc->nl_full[n & 7]), (n >> 3) & 1));
+        if (!ok) break;
+        tc_fence_after();
+        const int t0 = (tt0 + (it0 + it) / p.c.G) * 128 + side * 64;
+        const bool edge = (p.causal && base + t0 < key0 + 127) || t0 + 64 > s.q;
+        const float4* nl = reinterpret_cast<const float4*>(misc->nl[n & 7]) + side * 16;
+        // Two copies of the pass: only tiles at the diagonal or the end test their tokens.
+        total += edge ? weigh_tile<true>(s, tS + st * 128, nl, c, smem_addr(&misc->s_free[st]), t0, p.causal ? key - base : 0)
+                      : weigh_tile<false>(s, tS + st * 128, nl, c, smem_addr(&misc->s_free[st]), t0, 0);
+      }
+      if (side == 1) misc->half[row] = total;
+      named_bar_sync(1, C::SUM_THREADS);
+      if (side == 0 && ok && row < n_keys) {
+        total += misc->half[row];
+        const int64_t at = static_cast<int64_t>(bh) * p.n_weights + key;
+        if (p.parts > 1) p.part_w[static_cast<int64_t>(part) * bh_n * p.n_weights + at] = static_cast<float>(total);
+        else p.weights[at] = static_cast<float>(p.accumulate ? static_cast<double>(p.weights[at]) + total : total);
+      }
     }
+    cnt += max(0, n_it);
+    __syncthreads();  // every product that reads the keys is done, and the next item is there
+  }
+  // Every copy and product issued has ended before shared and tensor memory go away (after an abort some may be in flight).
+  if (warp == C::LOAD_WARP && lane == 0)
+    for (int n = max(0, copies - 2); n < copies; ++n) w.drain(smem_addr(&misc->q_full[n & 1]), (n >> 1) & 1);
+  if (warp == C::MMA_WARP) {
     if (leader) tc_commit(smem_addr(&misc->drain));
     __syncwarp();
     w.drain(smem_addr(&misc->drain), 0);
-  } else {  // one key per thread
-    const int key = key0 + tid;
-    const float c = p.scale_log2 * sf_of(p.sf_k, p.sf_k_kind, bh);
-    const uint32_t tS = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    double total = 0.0;  // 32 bits inside a tile, 64 across: a prompt's sum has tens of thousands of terms
-    bool ok = true;
-    for (int it = 0; it < n_it; ++it) {
-      const int st = it & 1;
-      const uint32_t ph = (it >> 1) & 1;
-      ok = __all_sync(kFull, w.wait(smem_addr(&misc->s_full[st]), ph)) &&
-           __all_sync(kFull, w.wait(smem_addr(&misc->nl_full[it & 7]), (it >> 3) & 1));
-      if (!ok) break;
-      tc_fence_after();
-      const int t0 = (tt0 + (it0 + it) / p.c.G) * 128;
-      const bool edge = (p.causal && base + t0 < key0 + 127) || t0 + 128 > s.q;
-      const float4* nl = reinterpret_cast<const float4*>(misc->nl[it & 7]);
-      // Two copies of the pass: only tiles at the diagonal or the end test their tokens.
-      total += edge ? weigh_tile<true>(p, s, tS + st * 128, nl, c, smem_addr(&misc->s_free[st]), t0, p.causal ? key - base : 0)
-                    : weigh_tile<false>(p, s, tS + st * 128, nl, c, smem_addr(&misc->s_free[st]), t0, 0);
-    }
-    if (ok && tid < n_keys) {
-      const int64_t at = static_cast<int64_t>(bh) * p.n_weights + key;
-      if (p.parts > 1) p.part_w[static_cast<int64_t>(part) * bh_n * p.n_weights + at] = static_cast<float>(total);
-      else p.weights[at] = static_cast<float>(p.accumulate ? static_cast<double>(p.weights[at]) + total : total);
-    }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 4) {
+  if (warp == C::MMA_WARP) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
@@ -467,6 +457,8 @@ template <int D, bool K8>
 cudaError_t launch_many(const KeyWeightsParams& p, const CUtensorMap& tq, cudaStream_t s) {
   auto kern = key_weights_many_kernel<D, K8>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, KmCfg<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  e = cudaMemsetAsync(p.ticket, 0, sizeof(uint32_t), s);
   if (e != cudaSuccess) return e;
   kern<<<p.n_ctas, KmCfg<D>::THREADS, KmCfg<D>::SMEM, s>>>(p, tq);
   e = cudaGetLastError();
