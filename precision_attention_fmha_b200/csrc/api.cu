@@ -430,7 +430,7 @@ fmha_status run_attention(const fmha_args* a, const uint8_t* mask, int64_t msb, 
     e = launch_attention_packed(qk, pv, paged, p, tq, tk, tv, to, stream);
     if (e != cudaSuccess) return fail(FMHA_ERR_CUDA, "decode attention launch: %s", cudaGetErrorString(e));
     if (sp.n_parts > 1) {
-      MergeParams mp = {};
+      MergeParams mp;
       mp.o_part = p.o_part;
       mp.lse_part = p.lse_part;
       mp.o = static_cast<uint16_t*>(a->o.ptr);

@@ -282,6 +282,7 @@ fmha_status packed_params(const fmha_cache_args* a, const CacheAttnParams& c, co
   p->kv_interleave = t.interleave;
   p->n_parts = t.n_parts;  // at least two: every tile writes a partial
   p->ctx_lens = c.c.lens;
+  p->q_lens = c.c.q_lens;
   p->o_part = c.part_o;
   p->lse_part = c.part_lse;
   p->p_terms = 1;
@@ -326,6 +327,7 @@ fmha_status fmha_fwd_tree(const fmha_cache_args* a, const uint8_t* tree_mask, in
   p.mask = tree_mask;
   p.mask_sb = mask_stride_b;
   p.row_tiles = t.row_tiles;
+  p.tile_rows = t.rows;
   p.n_ctas = t.n_ctas;
   p.min_tiles = kMinTiles;
   p.part_o = static_cast<float*>(workspace);
@@ -338,17 +340,7 @@ fmha_status fmha_fwd_tree(const fmha_cache_args* a, const uint8_t* tree_mask, in
     if ((st = packed_params(a, p, t, &ap, &tq, &tkp, &tvp)) != FMHA_OK) return st;
     e = launch_attention_packed(QK_BF16, PV_BF16, p.c.page_table != nullptr, ap, tq, tkp, tvp, tq, stream);
     if (e == cudaSuccess) e = launch_cache_tail(p, tk, tv, stream);
-    if (e == cudaSuccess) {
-      MergeParams m = {};
-      m.o_part = p.part_o;
-      m.lse_part = p.part_lse;
-      m.o = p.o;
-      m.o_sb = p.o_sb; m.o_ss = p.o_ss; m.o_sh = p.o_sh;
-      m.lse = p.lse;
-      m.n_splits = t.n_parts; m.B = a->B; m.Sq = a->T; m.Hq = a->Hq; m.D = a->D;
-      m.q_lens = p.c.q_lens;
-      e = launch_split_merge(m, stream);
-    }
+    if (e == cudaSuccess) e = launch_parts_merge(p, stream);
   } else {
     p.part_lse = p.part_o + size_t(2) * t.n_ctas * t.rows * a->D;
     e = launch_cache_attn(a->D, k8, v8, p, tk, tv, stream);
@@ -387,6 +379,7 @@ fmha_status fmha_fwd_selected(const fmha_cache_args* a, const int32_t* blocks, i
   p.block_shift = log2_of(block);
   p.n_blocks = ceil_div(p.c.capacity, block);
   p.row_tiles = t.row_tiles;
+  p.tile_rows = t.rows;
   p.n_ctas = t.n_ctas;
   p.item_tiles = t.item_tiles;
   p.n_splits = t.n_splits;

@@ -41,8 +41,7 @@ __global__ void __launch_bounds__(128) split_merge_kernel(const MergeParams m) {
   const long long split_stride_lse = static_cast<long long>(m.B) * m.Hq * m.Sq;
   const long long lse_off = (static_cast<long long>(b) * m.Hq + h) * m.Sq + tok;
   float mx = -INFINITY;
-  const bool hidden = m.q_lens != nullptr && tok >= __ldg(m.q_lens + b);
-  for (int j = lane; j < m.n_splits && !hidden; j += 32) mx = fmaxf(mx, m.lse_part[j * split_stride_lse + lse_off]);
+  for (int j = lane; j < m.n_splits; j += 32) mx = fmaxf(mx, m.lse_part[j * split_stride_lse + lse_off]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   float acc[4] = {0.f, 0.f, 0.f, 0.f};

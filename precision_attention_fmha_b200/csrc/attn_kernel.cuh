@@ -1485,6 +1485,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     item /= p.n_splits;
     hkv = item % p.Hkv;
     b = item / p.Hkv;
+    if (p.ctx_lens != nullptr && p.B <= 32) {
+      // Sequences of different lengths: the longest start first, so that the
+      // last CTAs to end are short ones (lane l ranks sequence l).
+      const int len = lane < p.B ? __ldg(p.ctx_lens + lane) : -1;
+      int before = 0;
+      for (int i = 0; i < p.B; ++i) {
+        const int other = __shfl_sync(0xffffffffu, len, i);
+        before += other > len || (other == len && i < lane);
+      }
+      b = __ffs(__ballot_sync(0xffffffffu, lane < p.B && before == b)) - 1;
+    }
     const int toks = C::BM >> p.group_shift;  // query tokens per 128-row unit
     for (int x = 0; x < 2; ++x) {
       t[x].h = hkv * p.group;
@@ -1498,7 +1509,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int last = min(t[x].tok0 + toks - 1, p.Sq - 1) + (p.Skv - p.Sq);
         n = last < 0 ? 0 : min(p.n_kv_blocks, last / C::BN + 1);
       }
-      if (p.ctx_lens != nullptr) n = min(max(__ldg(p.ctx_lens + b), 0) / C::BN, n);
+      if (p.ctx_lens != nullptr) {
+        n = min(max(__ldg(p.ctx_lens + b), 0) / C::BN, n);
+        if (p.q_lens != nullptr && t[x].tok0 >= __ldg(p.q_lens + b)) t[x].valid = false;  // padding rows only
+      }
       t[x].n_kv = t[x].valid ? n : 0;
       t[x].u0 = 0;
       t[x].x = x;

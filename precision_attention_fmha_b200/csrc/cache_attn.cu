@@ -113,12 +113,13 @@ __device__ __forceinline__ void load_v(uint32_t (&b)[4][2], uint32_t v_base, int
   }
 }
 
-// Whether a 16-bit pair holds an infinity or a NaN.
+// Bits 15 and 31 set where a half of a 16-bit pair is an infinity or a NaN (all exponent bits set: adding one carries).
 template <bool F16>
-__device__ __forceinline__ bool not_finite(uint32_t x) {
-  constexpr uint32_t E = F16 ? 0x7c00u : 0x7f80u;
-  return (x & E) == E || ((x >> 16) & E) == E;
+__device__ __forceinline__ uint32_t not_finite(uint32_t x) {
+  constexpr uint32_t E = F16 ? 0x7c007c00u : 0x7f807f80u, ONE = F16 ? 0x04000400u : 0x00800080u;
+  return (x & E) + ONE;
 }
+
 template <class C>
 __device__ void consume(const CacheAttnParams& p, uint8_t* ring, float* red, CaMisc<C::STAGES>* misc, const Waiter w) {
   using namespace ptx;
@@ -146,6 +147,10 @@ __device__ void consume(const CacheAttnParams& p, uint8_t* ring, float* red, CaM
       load_q<C::K8, KS, 4>(qf, h, cs[h], src, rows[h].tok >= 0, j);
       cs[h] *= p.scale_log2 * sfk;
     }
+    const uint8_t* mask_row[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      mask_row[h] = p.mask + (C::PICKED ? 0 : g.b * p.mask_sb + static_cast<int64_t>(max(rows[h].tok, 0)) * p.c.T);
     float acc[NQ * 4][4];
 #pragma unroll
     for (int i = 0; i < NQ * 4; ++i)
@@ -198,6 +203,7 @@ __device__ void consume(const CacheAttnParams& p, uint8_t* ring, float* red, CaM
         if (!plain) {  // hide keys: past the end, or nodes this row does not see
 #pragma unroll
           for (int i = 0; i < GPW; ++i) {
+            if (valid[i] == 16 && pos[i] + 16 <= g.ctx) continue;
             uint32_t show = 0xffu;  // bit 4 x + e of the group's sc[2 i + x][e]
             if constexpr (!C::PICKED) {
               const int node0 = pos[i] - g.ctx;  // node of the group's first key
@@ -208,8 +214,7 @@ __device__ void consume(const CacheAttnParams& p, uint8_t* ring, float* red, CaM
                   const int node = node0 + (e >> 2) * 8 + 2 * j + (e & 1), tok = rows[(e >> 1) & 1].tok;
                   bool see = node < 0 || (tok >= 0 && node <= tok);
                   if (p.mask != nullptr) {
-                    const uint8_t byte = __ldg(p.mask + g.b * p.mask_sb + static_cast<int64_t>(max(tok, 0)) * p.c.T +
-                                               min(max(node, 0), p.c.T - 1));
+                    const uint8_t byte = __ldg(mask_row[(e >> 1) & 1] + min(max(node, 0), p.c.T - 1));
                     see = node < 0 || (tok >= 0 && byte != 0);
                   }
                   show |= see ? 1u << e : 0u;
@@ -267,7 +272,7 @@ __device__ void consume(const CacheAttnParams& p, uint8_t* ring, float* red, CaM
           for (int q = 0; q < NQ; ++q) {
             uint32_t b[4][2];
             load_v<C>(b, v_base, key0, q, lane);
-            if (!plain) {
+            if (!plain && !(valid[i] == 16 && pos[i] + 16 <= g.ctx)) {
               // Rows past the end hold anything: they count as zero. A node
               // that some row does not see may hold infinities or NaN, which a
               // zero weight would not stop: such a group adds key by key.
@@ -275,15 +280,20 @@ __device__ void consume(const CacheAttnParams& p, uint8_t* ring, float* red, CaM
 #pragma unroll
               for (int h = 0; h < 2; ++h)
                 keep[h] = (2 * j + 8 * h < valid[i] ? 0xffffu : 0u) | (2 * j + 1 + 8 * h < valid[i] ? 0xffff0000u : 0u);
-              bool odd = false;
+              if (valid[i] < 16) {
 #pragma unroll
-              for (int n = 0; n < 4; ++n)
+                for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  b[n][h] &= keep[h];
-                  odd = odd || not_finite<C::V8>(b[n][h]);
-                }
-              if (__any_sync(kFull, odd)) {
+                  for (int h = 0; h < 2; ++h) b[n][h] &= keep[h];
+              }
+              uint32_t odd = 0u;
+              if constexpr (!C::PICKED) {
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) odd |= not_finite<C::V8>(b[n][h]);
+              }
+              if (__any_sync(kFull, odd & 0x80008000u)) {
 #pragma unroll 1
                 for (int k = 0; k < 16; ++k) {
                   const int from = (lane & ~3) | ((k & 7) >> 1);
@@ -639,15 +649,15 @@ __device__ void consume_t(const CacheAttnParams& p, uint8_t* ring, float* red, C
 #pragma unroll
             for (int h = 0; h < 2; ++h)
               keep[h] = (2 * j + 8 * h < valid ? 0xffffu : 0u) | (2 * j + 1 + 8 * h < valid ? 0xffff0000u : 0u);
-            bool odd = false;
+            uint32_t odd = 0u;
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 a[t][i] &= keep[i >> 1];
-                odd = odd || not_finite<C::V8>(a[t][i]);
+                odd |= not_finite<C::V8>(a[t][i]);
               }
-            if (__any_sync(kFull, odd)) {
+            if (__any_sync(kFull, odd & 0x80008000u)) {
 #pragma unroll 1
               for (int k = 0; k < 16; ++k) {
                 const int from_p = (k & 7) * 4 + j, from_v = (lane & ~3) | ((k & 7) >> 1);
@@ -885,6 +895,62 @@ __global__ void __launch_bounds__(128) cache_merge_kernel(const __grid_constant_
     *lse_out = sum != 0.f ? (mx + __log2f(sum)) * 0.69314718055994531f : -INFINITY;
 }
 
+// Joins the parts of a packed call's rows (D = 128). Two rows per warp, 16 lanes
+// of 8 columns each; a row's parts are loaded before their weights are known,
+// so a row costs one memory latency (65536 rows of 3 parts: 73 us with the
+// weights first, 30 us so).
+__global__ void __launch_bounds__(256) parts_merge_kernel(const __grid_constant__ CacheAttnParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int half = (threadIdx.x >> 4) & 1, l16 = threadIdx.x & 15;
+  const long long rows = static_cast<long long>(p.c.B) * p.c.T * p.c.Hq;
+  const long long row = (static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * 2 + half;
+  if (row >= rows) return;
+  const int h = static_cast<int>(row % p.c.Hq);
+  const long long bt = row / p.c.Hq;
+  const int tok = static_cast<int>(bt % p.c.T), b = static_cast<int>(bt / p.c.T);
+  const int n = p.tail_part + 1;
+  const long long lse_at = (static_cast<long long>(b) * p.c.Hq + h) * p.c.T + tok;
+  bool bad;
+  const bool hidden = tok >= tree_lens(p.c, b, bad).q;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  float m = -INFINITY, sum = 0.f;
+  for (int k0 = 0; k0 < n && !hidden; k0 += 4) {
+    float lse[4];
+    float4 v[4][2];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool live = k0 + k < n;
+      lse[k] = live ? __ldg(p.part_lse + (k0 + k) * rows + lse_at) : -INFINITY;
+      const float4* src = reinterpret_cast<const float4*>(p.part_o + ((k0 + k) * rows + row) * 128 + l16 * 8);
+      v[k][0] = live ? __ldg(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[k][1] = live ? __ldg(src + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float mn = m;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mn = fmaxf(mn, lse[k]);
+    const float mb = mn == -INFINITY ? 0.f : mn;
+    const float f = m == mn ? 1.f : expf(m - mb);
+    m = mn;
+    sum *= f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] *= f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (lse[k] == -INFINITY) continue;  // a part that saw no key
+      const float w = expf(lse[k] - mb);
+      sum += w;
+      const float x[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w, v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, x[e], acc[e]);
+    }
+  }
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
+  *reinterpret_cast<uint4*>(p.o + b * p.o_sb + tok * p.o_ss + h * p.o_sh + l16 * 8) =
+      make_uint4(ptx::pack_bf16x2(acc[0] * inv, acc[1] * inv), ptx::pack_bf16x2(acc[2] * inv, acc[3] * inv),
+                 ptx::pack_bf16x2(acc[4] * inv, acc[5] * inv), ptx::pack_bf16x2(acc[6] * inv, acc[7] * inv));
+  if (p.lse != nullptr && l16 == 0) p.lse[lse_at] = sum != 0.f ? m + logf(sum) : -INFINITY;
+}
+
 template <class C>
 cudaError_t launch_cfg(const CacheAttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
   auto kern = cache_attn_kernel<C>;
@@ -960,6 +1026,20 @@ cudaError_t launch_cache_merge(int D, const CacheAttnParams& p, cudaStream_t s) 
                    : cudaLaunchKernelEx(&cfg, cache_merge_kernel<128, true>, p, rows);
   return D == 64 ? cudaLaunchKernelEx(&cfg, cache_merge_kernel<64, false>, p, rows)
                  : cudaLaunchKernelEx(&cfg, cache_merge_kernel<128, false>, p, rows);
+}
+
+cudaError_t launch_parts_merge(const CacheAttnParams& p, cudaStream_t s) {
+  const long long rows = static_cast<long long>(p.c.B) * p.c.T * p.c.Hq;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + 15) / 16));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, parts_merge_kernel, p);
 }
 
 }  // namespace fmha

@@ -23,7 +23,7 @@ struct CacheView {
 struct CacheParams {
   CacheView c;
   int32_t piece_shift;        // log2 of the rows of one TMA copy (16, 32 or 64)
-  int32_t row_tiles;          // tiles of query rows per KV head
+  int32_t row_tiles, tile_rows;  // tiles of query rows per KV head, and rows of one
   int32_t n_ctas, min_tiles;  // grid, and the least key tiles a CTA takes
   // picked blocks: [B, T, Hkv, top], a negative id is no block; key tiles of an item, and how CTAs share them
   const int32_t* blocks;
@@ -54,6 +54,8 @@ constexpr int cache_attn_ctas(int rows) { return rows <= 8 ? 3 : 2; }
 cudaError_t launch_cache_attn(int D, bool k8, bool v8, const CacheAttnParams& p, const CUtensorMap& tk,
                               const CUtensorMap& tv, cudaStream_t stream);
 cudaError_t launch_cache_tail(const CacheAttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream);
+// D = 128: joins the tail_part + 1 parts of each row.
+cudaError_t launch_parts_merge(const CacheAttnParams& p, cudaStream_t stream);
 cudaError_t launch_cache_merge(int D, const CacheAttnParams& p, cudaStream_t stream);
 
 // Attention weight that each cached key gathers over the query tokens.

@@ -208,7 +208,8 @@ struct Walk {
       g.nodes = s.q;
       g.first = s.len & ~127;
       g.limit = s.len + s.q;
-      g.nt = (g.limit - g.first + kTileKeys - 1) / kTileKeys;
+      // a row tile of padding rows alone has nothing to do
+      g.nt = g.rt * p.tile_rows < s.q * p.c.G ? (g.limit - g.first + kTileKeys - 1) / kTileKeys : 0;
       g.t0 = 0;
       g.t1 = g.nt;
     } else {

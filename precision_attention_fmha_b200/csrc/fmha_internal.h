@@ -72,6 +72,7 @@ struct AttnParams {
   // Packed, nullable [B]: sequence b has only its first ctx_lens[b] / 128 whole
   // key tiles here (the rest is another kernel's); Skv then bounds them all.
   const int32_t* ctx_lens;
+  const int32_t* q_lens;  // with ctx_lens, nullable [B]: query tokens in use; a tile of later ones writes nothing
   float* o_part;   // [n_parts, B, Sq, Hq, D] when n_parts > 1
   float* lse_part; // [n_parts, B, Hq, Sq]
   uint32_t* err;        // device error word
@@ -112,7 +113,6 @@ struct MergeParams {
   uint16_t* o; int64_t o_sb, o_ss, o_sh;  // bf16 bits
   float* lse;                             // nullable [B, Hq, Sq]
   int32_t n_splits, B, Sq, Hq, D;
-  const int32_t* q_lens;                  // nullable [B]: rows of later tokens give O = 0, lse = -inf
 };
 cudaError_t launch_split_merge(const MergeParams& m, cudaStream_t stream);
 
