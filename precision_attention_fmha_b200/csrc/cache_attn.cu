@@ -369,6 +369,76 @@ __device__ void consume(const CacheAttnParams& p, uint8_t* ring, float* red, CaM
     }
     const bool whole = g.t0 == 0 && g.t1 == g.nt;
     const int64_t slot = 2ll * blockIdx.x + (g.t0 == 0 ? 1 : 0);
+    if constexpr (C::WN == 1) {
+      // A warp has its rows to itself and writes them from its registers, 16 bytes and more of a row at a time.
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const Row ro = rows[h];
+        const int item_row = wm * 16 + gq + 8 * h;
+        const bool mine = ro.tok >= 0 && ok;
+        float M, L;
+        total(wm, gq + 8 * h, M, L);
+        const float lse = L != 0.f ? M + __log2f(L) : -INFINITY;
+        if (C::TAIL || !whole) {
+          const int64_t at = C::TAIL ? ((static_cast<int64_t>(p.tail_part) * p.c.B + g.b) * p.c.T + ro.tok) * p.c.Hq + ro.head
+                                     : slot * C::ROWS + item_row;
+          float* dst = p.part_o + at * D;
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            if constexpr (C::V8) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (mine)
+                  *reinterpret_cast<float4*>(dst + 32 * q + 8 * j + 4 * e) =
+                      make_float4(acc[4 * q][2 * h + e] * f[h], acc[4 * q + 1][2 * h + e] * f[h],
+                                  acc[4 * q + 2][2 * h + e] * f[h], acc[4 * q + 3][2 * h + e] * f[h]);
+            } else {
+#pragma unroll
+              for (int n = 0; n < 4; ++n)
+                if (mine)
+                  *reinterpret_cast<float2*>(dst + 32 * q + 8 * n + 2 * j) =
+                      make_float2(acc[4 * q + n][2 * h] * f[h], acc[4 * q + n][2 * h + 1] * f[h]);
+            }
+          }
+          if (mine && j == 0) {
+            if constexpr (C::TAIL)
+              p.part_lse[((static_cast<int64_t>(p.tail_part) * p.c.B + g.b) * p.c.Hq + ro.head) * p.c.T + ro.tok] =
+                  lse * 0.69314718055994531f;
+            else p.part_lse[at] = lse;
+          }
+        } else {
+          const bool hide = !C::PICKED && ro.tok >= g.nodes;  // a padding row: its factor may be anything
+          uint16_t* dst = p.o + g.b * p.o_sb + ro.tok * p.o_ss + ro.head * p.o_sh;
+          auto pair = [&](float x, float y) { return hide ? 0u : pack_bf16x2(x * f[h], y * f[h]); };
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            if constexpr (C::V8) {
+              if (mine)
+                *reinterpret_cast<uint4*>(dst + 32 * q + 8 * j) =
+                    make_uint4(pair(acc[4 * q][2 * h], acc[4 * q + 1][2 * h]), pair(acc[4 * q + 2][2 * h], acc[4 * q + 3][2 * h]),
+                               pair(acc[4 * q][2 * h + 1], acc[4 * q + 1][2 * h + 1]),
+                               pair(acc[4 * q + 2][2 * h + 1], acc[4 * q + 3][2 * h + 1]));
+            } else {
+              // Even lanes collect four columns of the first n-tile, odd lanes of the second: 32 bytes per four lanes.
+#pragma unroll
+              for (int n = 0; n < 4; n += 2) {
+                const uint32_t x = pair(acc[4 * q + n][2 * h], acc[4 * q + n][2 * h + 1]);
+                const uint32_t y = pair(acc[4 * q + n + 1][2 * h], acc[4 * q + n + 1][2 * h + 1]);
+                const uint32_t other = __shfl_xor_sync(kFull, (j & 1) ? x : y, 1);
+                if (mine)
+                  *reinterpret_cast<uint2*>(dst + 32 * q + 8 * (n + (j & 1)) + 4 * (j >> 1)) =
+                      (j & 1) ? make_uint2(other, y) : make_uint2(x, other);
+              }
+            }
+          }
+          if (mine && j == 0 && p.lse != nullptr)
+            p.lse[(static_cast<int64_t>(g.b) * p.c.Hq + ro.head) * p.c.T + ro.tok] =
+                hide ? -INFINITY : lse * 0.69314718055994531f;
+        }
+      }
+      __syncwarp();  // the next item's (m, l) may be written
+      continue;
+    }
     // Lanes that write: WN > 1: 8 per row over all 128 threads; else 8 per row of the warp.
     const int tid = C::WN > 1 ? threadIdx.x : lane;
     constexpr int PASS_ROWS = C::WN > 1 ? 16 : 4, PASSES = (C::WN > 1 ? C::ROWS : 16) / PASS_ROWS;
