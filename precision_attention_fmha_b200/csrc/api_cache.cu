@@ -552,7 +552,7 @@ fmha_status fmha_evict_select(const fmha_cache_args* a, const float* weights, in
     return fail(FMHA_ERR_INVALID_ARG, "weights is NULL or misaligned");
   if (keep == nullptr || counts == nullptr || ((reinterpret_cast<uintptr_t>(keep) | reinterpret_cast<uintptr_t>(counts)) & 3u))
     return fail(FMHA_ERR_INVALID_ARG, "keep or counts is NULL or misaligned");
-  if (static_cast<int64_t>(a->B) * a->Hkv >= (int64_t(1) << 31)) return fail(FMHA_ERR_UNSUPPORTED, "grid too large");
+  if (static_cast<int64_t>(a->B) * a->Hkv >= (int64_t(1) << 28)) return fail(FMHA_ERR_UNSUPPORTED, "grid too large");
   if (n_weights > INT32_MAX / 2 || budget > INT32_MAX / 2)
     return fail(FMHA_ERR_UNSUPPORTED, "more than 2^30 tokens per sequence");
   EvictParams p;

@@ -21,7 +21,9 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 constexpr int kEvictThreads = 1024, kEvictWarps = kEvictThreads / 32;
 
 // One CTA per (sequence, KV head): the `left`-th largest weight digit by digit
-// (11 + 11 + 10 bits), then the kept positions in ascending order.
+// (11 + 11 + 10 bits), then the kept positions in ascending order. 64 heads of
+// 32768 weights take 27 us; four CTAs a head, joining their counters over
+// distributed shared memory, took 35 us (eight cluster barriers).
 // CACHED: the keys stay in shared memory between the passes.
 constexpr int kEvictCached = 49152;  // keys
 template <bool CACHED>

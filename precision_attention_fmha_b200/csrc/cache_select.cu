@@ -117,24 +117,6 @@ __global__ void __launch_bounds__(256) key_bounds_kernel(const __grid_constant__
 }
 
 // ------------------------------------------------------------ score and pick --
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// Address of the same shared-memory variable in CTA 0 of the cluster.
-__device__ __forceinline__ uint32_t in_cta0(uint32_t addr) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
-  return r;
-}
-__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-
 // Order like the numbers (a larger score has a larger key; -0 counts as +0).
 __device__ __forceinline__ unsigned long long order_key(double x) {
   const long long v = __double_as_longlong(x + 0.0);
@@ -336,7 +318,7 @@ __global__ void __launch_bounds__(kPickThreads) select_blocks_kernel(const __gri
 #pragma unroll
     for (int e = 0; e < 8; ++e) w[e] = m->half[(in * 8 + e) / D][(in * 8 + e) % D];
     const int stride = kPickWarps * p.cluster * BPW;
-    const uint32_t dst = p.cluster > 1 ? in_cta0(ptx::smem_addr(keys)) : ptx::smem_addr(keys);
+    const uint32_t dst = p.cluster > 1 ? in_cta(ptx::smem_addr(keys), 0) : ptx::smem_addr(keys);
     float worst = 0.f;
     for (int j = f0 + (rank * kPickWarps + warp) * BPW + lane / LPB; j - lane / LPB < f1; j += 4 * stride) {
       uint4 v[4];
@@ -387,7 +369,7 @@ __global__ void __launch_bounds__(kPickThreads) select_blocks_kernel(const __gri
         worst = larger(worst, __int_as_float(m->warp_a[i]));
       }
       const float e = worst * (1.5f * 0x1p-24f) * static_cast<float>(rows + 32);
-      if (p.cluster > 1) st_cluster(in_cta0(ptx::smem_addr(&m->err[rank])), __float_as_uint(e));
+      if (p.cluster > 1) st_cluster(in_cta(ptx::smem_addr(&m->err[rank]), 0), __float_as_uint(e));
       else m->err[0] = e;
     }
     if (p.cluster > 1) cluster_sync();

@@ -414,12 +414,14 @@ class _launch:
 
     __slots__ = ("contexts", "stream", "device")
 
-    def __init__(self, stream, *tensors):
-        devices = {t.get_device() for t in tensors if t is not None}
-        device = devices.pop()
-        if devices or device < 0:
+    def __init__(self, stream, first, *tensors):
+        device = first.get_device()
+        for t in tensors:
+            if t is not None and t.get_device() != device:
+                device = -1
+        if device < 0:
             raise ValueError("all tensors must be on one CUDA device, got "
-                             f"{sorted({str(t.device) for t in tensors if t is not None})}")
+                             f"{sorted({str(t.device) for t in (first, *tensors) if t is not None})}")
         if stream is not None and stream.device.index != device:
             raise ValueError(f"stream of {stream.device} for tensors of cuda:{device}")
         self.stream, self.device, self.contexts = stream, device, ()
@@ -427,15 +429,23 @@ class _launch:
     def __enter__(self):
         if self.device != torch.cuda.current_device():
             self.contexts += (torch.cuda.device(self.device),)
-        if self.stream is not None:
+        if self.stream is None:
+            if not self.contexts:
+                return _raw_stream(self.device)
+        else:
             self.contexts += (torch.cuda.stream(self.stream),)
         for c in self.contexts:
             c.__enter__()
-        return (self.stream or torch.cuda.current_stream(self.device)).cuda_stream
+        return _raw_stream(self.device)
 
     def __exit__(self, *exc):
         for c in reversed(self.contexts):
             c.__exit__(*exc)
+
+
+def _raw_stream(device):
+    """Handle of the device's current stream (a tenth of the time that making a torch Stream takes)."""
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _array(t, dtype, shape, what):
@@ -518,15 +528,10 @@ def _scratch(workspace, need, q):
     if workspace is None:
         if need == 0:
             return None, 0, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = q.new_empty(need, dtype=torch.uint8)
     elif workspace.get_device() != q.get_device():
         raise ValueError(f"workspace on {workspace.device}, tensors on {q.device}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
-
-
-def _out_for(q, out):
-    """O like q, when the caller gives none: its output must be in the arguments before they are packed."""
-    return torch.empty(q.shape, dtype=torch.bfloat16, device=q.device) if out is None else out
 
 
 def _sf_tensors(*scales):
@@ -553,7 +558,7 @@ def fmha_fwd_tree(q, k, v, ctx_lens, tree_mask=None, tree_lens=None, page_table=
         mask, mask_sb = tree_mask.data_ptr(), st[0] if tree_mask.shape[0] > 1 else 0
     lib = load_library()
     with _launch(stream, q, k, v, ctx_lens, tree_mask, tree_lens, page_table, out, lse, *_sf_tensors(sf_k, sf_v)) as s:
-        out = _out_for(q, out)
+        out = q.new_empty(q.shape, dtype=torch.bfloat16) if out is None else out
         a, _ = _cache_args(k, ctx_lens, page_table, q=q, v=v, out=out, q_lens=tree_lens, sf_k=sf_k, sf_v=sf_v,
                            softmax_scale=softmax_scale, lse=lse)
         workspace, ptr, size = _scratch(workspace, lib.fmha_fwd_tree_workspace_bytes(a), q)
@@ -580,7 +585,7 @@ def fmha_fwd_selected(q, k, v, blocks, lens, block, q_lens=None, page_table=None
     ids = _ints(blocks, (q.shape[0], q.shape[1], k.shape[2], top), "blocks")
     lib = load_library()
     with _launch(stream, q, k, v, blocks, lens, q_lens, page_table, out, lse, *_sf_tensors(sf_k, sf_v)) as s:
-        out = _out_for(q, out)
+        out = q.new_empty(q.shape, dtype=torch.bfloat16) if out is None else out
         a, _ = _cache_args(k, lens, page_table, q=q, v=v, out=out, q_lens=q_lens, sf_k=sf_k, sf_v=sf_v,
                            softmax_scale=softmax_scale, lse=lse)
         workspace, ptr, size = _scratch(workspace, lib.fmha_fwd_selected_workspace_bytes(a, top, int(block)), q)
@@ -633,7 +638,7 @@ def select_blocks(q, bounds, lens, block, top, sink_blocks=0, recent_blocks=1, q
     lib = load_library()
     with _launch(stream, q, bounds, lens, q_lens, out) as s:
         if out is None:
-            out = torch.empty([max(0, n) for n in shape], dtype=dtype, device=q.device)
+            out = q.new_empty([max(0, n) for n in shape], dtype=dtype)
         _check(lib.fmha_select_blocks(a, bounds.data_ptr(), n_blocks, int(block), int(top),
                                       int(sink_blocks), int(recent_blocks), int(q_tile), out.data_ptr(), s))
     return out
@@ -675,9 +680,9 @@ def evict_select(weights, lens, budget, sinks=0, recent=0, keep=None, counts=Non
     lib = load_library()
     with _launch(stream, weights, lens, keep, counts) as s:
         if keep is None:
-            keep = torch.empty((B, Hkv, max(0, budget)), dtype=torch.int32, device=weights.device)
+            keep = weights.new_empty((B, Hkv, max(0, budget)), dtype=torch.int32)
         if counts is None:
-            counts = torch.empty((B,), dtype=torch.int32, device=weights.device)
+            counts = weights.new_empty((B,), dtype=torch.int32)
         _check(lib.fmha_evict_select(a, w, n, int(budget), int(sinks), int(recent), keep.data_ptr(),
                                      counts.data_ptr(), s))
     return keep, counts

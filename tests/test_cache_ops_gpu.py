@@ -177,6 +177,8 @@ def test_weights(B, T, Hq, Hkv, D, lens, page, kv, causal):
 @pytest.mark.parametrize("B,Hkv,lens,budget,sinks,recent", [
     (1, 1, [1], 1, 0, 0), (2, 2, [100, 5], 10, 2, 3), (1, 3, [5000], 1000, 4, 64), (3, 1, [33, 32, 31], 32, 0, 32),
     (1, 2, [40000], 7, 0, 0), (2, 1, [3000, 0], 2999, 1, 1), (1, 1, [70], 8, 4, 4),
+    (1, 1, [120000], 30001, 16, 100), (3, 8, [9000, 20000, 8193], 8192, 1, 0), (40, 4, [600 + i for i in range(40)], 601, 0, 1),
+    (160, 1, [60000] * 160, 100, 1, 1),  # too many keys for shared memory
 ])
 def test_evict_select(B, Hkv, lens, budget, sinks, recent):
     from precision_attention_fmha_b200 import fmha
