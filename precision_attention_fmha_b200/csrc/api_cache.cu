@@ -79,6 +79,11 @@ fmha_status check_cache(const fmha_cache_args* a, bool need_q, bool need_v, Cach
   c->num_pages = a->num_pages;
   c->page_shift = a->page_table != nullptr ? log2_of(a->page_size) : 0;
   c->max_pages = a->max_pages_per_seq;
+  return FMHA_OK;
+}
+
+// The current device's part of a view; after all argument checks.
+fmha_status bind_device(CacheView* c) {
   cudaError_t e;
   c->err = device_error_word(&e);
   if (c->err == nullptr) return fail(FMHA_ERR_CUDA, "device error word: %s", cudaGetErrorString(e));
@@ -231,9 +236,8 @@ int pick_cluster(int64_t items, int n_blocks) {
   return c;
 }
 
-// Fills what the tree and the picked form share, with the TMA maps.
-fmha_status fill_attn(const fmha_cache_args* a, CacheAttnParams* p, bool* k8, bool* v8, int piece, CUtensorMap* tk,
-                      CUtensorMap* tv) {
+// Checks and fills what the tree and the picked form share.
+fmha_status fill_attn(const fmha_cache_args* a, CacheAttnParams* p, bool* k8, bool* v8, int piece) {
   fmha_status st;
   memset(p, 0, sizeof(*p));
   if ((st = check_cache(a, true, true, &p->c, k8, v8)) != FMHA_OK) return st;
@@ -251,6 +255,13 @@ fmha_status fill_attn(const fmha_cache_args* a, CacheAttnParams* p, bool* k8, bo
   piece = std::min(piece, kTile);
   if (p->c.page_table != nullptr) piece = std::min(piece, a->page_size);
   p->piece_shift = log2_of(piece);
+  return FMHA_OK;
+}
+
+// The device's part: the error word and the TMA maps.
+fmha_status bind_attn(const fmha_cache_args* a, CacheAttnParams* p, bool k8, bool v8, CUtensorMap* tk, CUtensorMap* tv) {
+  fmha_status st;
+  if ((st = bind_device(&p->c)) != FMHA_OK) return st;
   if (p->c.capacity == 0) {  // no key is ever loaded; any valid map will do
     const uint64_t dims[4] = {uint64_t(a->D), 1, 1, 1};
     const int64_t strides[3] = {a->D, a->D, a->D};
@@ -259,8 +270,9 @@ fmha_status fill_attn(const fmha_cache_args* a, CacheAttnParams* p, bool* k8, bo
     *tv = *tk;
     return FMHA_OK;
   }
-  if ((st = cache_map(tk, a, p->c, a->k, *k8, piece, "k")) != FMHA_OK) return st;
-  return cache_map(tv, a, p->c, a->v, *v8, piece, "v");
+  const int piece = 1 << p->piece_shift;
+  if ((st = cache_map(tk, a, p->c, a->k, k8, piece, "k")) != FMHA_OK) return st;
+  return cache_map(tv, a, p->c, a->v, v8, piece, "v");
 }
 
 // The packed kernel's parameters for the contexts' whole 128-key tiles: every row sees every key of them, and every
@@ -320,10 +332,11 @@ fmha_status fmha_fwd_tree(const fmha_cache_args* a, const uint8_t* tree_mask, in
   CUtensorMap tk, tv;
   bool k8, v8;
   fmha_status st;
-  if ((st = fill_attn(a, &p, &k8, &v8, kTile, &tk, &tv)) != FMHA_OK) return st;
+  if ((st = fill_attn(a, &p, &k8, &v8, kTile)) != FMHA_OK) return st;
   TreePlan t;
   if (!tree_plan(a, p.c.capacity, &t)) return fail(FMHA_ERR_UNSUPPORTED, "grid too large");
   if ((st = check_workspace(workspace, workspace_bytes, t.workspace_bytes)) != FMHA_OK) return st;
+  if ((st = bind_attn(a, &p, k8, v8, &tk, &tv)) != FMHA_OK) return st;
   p.mask = tree_mask;
   p.mask_sb = mask_stride_b;
   p.row_tiles = t.row_tiles;
@@ -370,10 +383,11 @@ fmha_status fmha_fwd_selected(const fmha_cache_args* a, const int32_t* blocks, i
   CacheAttnParams p;
   CUtensorMap tk, tv;
   bool k8, v8;
-  if ((st = fill_attn(a, &p, &k8, &v8, block, &tk, &tv)) != FMHA_OK) return st;
+  if ((st = fill_attn(a, &p, &k8, &v8, block)) != FMHA_OK) return st;
   PickPlan t;
   if (!pick_plan(a, top, block, &t)) return fail(FMHA_ERR_UNSUPPORTED, "grid too large");
   if ((st = check_workspace(workspace, workspace_bytes, t.workspace_bytes)) != FMHA_OK) return st;
+  if ((st = bind_attn(a, &p, k8, v8, &tk, &tv)) != FMHA_OK) return st;
   p.blocks = blocks;
   p.top = top;
   p.block_shift = log2_of(block);
@@ -407,6 +421,7 @@ fmha_status fmha_key_bounds(const fmha_cache_args* a, void* bounds, int32_t n_bl
   if ((st = check_cache(a, false, false, &p.c, &k8, &v8)) != FMHA_OK) return st;
   if (static_cast<int64_t>(a->B) * a->Hkv * n_blocks >= (int64_t(1) << 33))
     return fail(FMHA_ERR_UNSUPPORTED, "grid too large");
+  if ((st = bind_device(&p.c)) != FMHA_OK) return st;
   p.k = static_cast<const uint8_t*>(a->k.ptr);
   p.k_sb = a->k.stride_b; p.k_ss = a->k.stride_s; p.k_sh = a->k.stride_h;
   p.bounds = static_cast<uint16_t*>(bounds);
@@ -438,6 +453,7 @@ fmha_status fmha_select_blocks(const fmha_cache_args* a, const void* bounds, int
   if ((st = check_tensor(a->q, "q", a->B, a->T, a->Hq, a->D)) != FMHA_OK) return st;
   if (n_blocks > 0 && (bounds == nullptr || !aligned16(bounds)))
     return fail(FMHA_ERR_INVALID_ARG, "bounds is NULL or not 16-byte aligned");
+  if (q_tile == 128 && n_blocks == 0) return ok_status();  // an empty mask
   if (picked == nullptr || (q_tile == 1 && (reinterpret_cast<uintptr_t>(picked) & 3u)))
     return fail(FMHA_ERR_INVALID_ARG, "picked is NULL or misaligned");
   if (a->lens == nullptr || (reinterpret_cast<uintptr_t>(a->lens) & 3u))
@@ -454,9 +470,7 @@ fmha_status fmha_select_blocks(const fmha_cache_args* a, const void* bounds, int
   p.c.capacity = n_blocks * block;
   p.c.lens = a->lens;
   p.c.q_lens = a->q_lens;
-  cudaError_t e;
-  p.c.err = device_error_word(&e);
-  if (p.c.err == nullptr) return fail(FMHA_ERR_CUDA, "device error word: %s", cudaGetErrorString(e));
+  if ((st = bind_device(&p.c)) != FMHA_OK) return st;
   p.q = static_cast<const uint16_t*>(a->q.ptr);
   p.q_sb = a->q.stride_b; p.q_ss = a->q.stride_s; p.q_sh = a->q.stride_h;
   p.bounds = static_cast<const uint16_t*>(bounds);
@@ -468,7 +482,7 @@ fmha_status fmha_select_blocks(const fmha_cache_args* a, const void* bounds, int
   p.cluster = pick_cluster(items, n_blocks);
   if (q_tile == 1) p.list = static_cast<int32_t*>(picked);
   else p.mask = static_cast<uint8_t*>(picked);
-  e = launch_select_blocks(a->D, p, stream);
+  cudaError_t e = launch_select_blocks(a->D, p, stream);
   if (e != cudaSuccess) return fail(FMHA_ERR_CUDA, "block selection launch: %s", cudaGetErrorString(e));
   return ok_status();
 }
@@ -513,6 +527,7 @@ fmha_status fmha_key_weights(const fmha_cache_args* a, float* weights, int32_t n
     const int64_t n = heads * ceil_div(std::min(p.c.capacity, n_weights), 128) * r.parts;
     if (n >= (int64_t(1) << 31) || heads > 65535) return fail(FMHA_ERR_UNSUPPORTED, "grid too large");
     if ((st = check_workspace(workspace, workspace_bytes, weight_bytes(a, r, n_weights))) != FMHA_OK) return st;
+    if ((st = bind_device(&p.c)) != FMHA_OK) return st;
     p.n_ctas = static_cast<int>(std::min<int64_t>(n, 2 * sm_count()));
     p.n_items = static_cast<uint32_t>(n);
     p.chunk = r.chunk;
@@ -526,6 +541,7 @@ fmha_status fmha_key_weights(const fmha_cache_args* a, float* weights, int32_t n
     e = launch_key_weights_many(a->D, k8, p, m, stream);
   } else {
     const int piece = p.c.page_table != nullptr ? std::min(kTile, a->page_size) : kTile;
+    if ((st = bind_device(&p.c)) != FMHA_OK) return st;
     if ((st = cache_map(&m, a, p.c, a->k, k8, piece, "k")) != FMHA_OK) return st;
     p.piece_shift = log2_of(piece);
     p.row_tiles = 1;
@@ -560,15 +576,14 @@ fmha_status fmha_evict_select(const fmha_cache_args* a, const float* weights, in
   p.c.B = a->B; p.c.Hkv = a->Hkv;
   p.c.capacity = a->capacity > 0 ? a->capacity : n_weights;
   p.c.lens = a->lens;
-  cudaError_t e;
-  p.c.err = device_error_word(&e);
-  if (p.c.err == nullptr) return fail(FMHA_ERR_CUDA, "device error word: %s", cudaGetErrorString(e));
+  fmha_status st;
+  if ((st = bind_device(&p.c)) != FMHA_OK) return st;
   p.weights = weights;
   p.n_weights = n_weights;
   p.budget = budget; p.sinks = sinks; p.recent = recent;
   p.keep = keep;
   p.counts = counts;
-  e = launch_evict_select(p, stream);
+  cudaError_t e = launch_evict_select(p, stream);
   if (e != cudaSuccess) return fail(FMHA_ERR_CUDA, "eviction launch: %s", cudaGetErrorString(e));
   return ok_status();
 }
@@ -626,6 +641,7 @@ fmha_status fmha_cache_compact(const fmha_cache_args* a, const fmha_cache_args* 
   const int64_t heads = static_cast<int64_t>(a->B) * a->Hkv;
   if (heads > INT32_MAX || heads * (ceil_div(std::max(n_keep, n_weights_out), 8) + 1) >= (int64_t(1) << 33))
     return fail(FMHA_ERR_UNSUPPORTED, "grid too large");
+  if ((st = bind_device(&p.c)) != FMHA_OK) return st;
   const int ek = k8 ? 1 : 2, ev = v8 ? 1 : 2;
   p.k = static_cast<const uint8_t*>(a->k.ptr); p.v = static_cast<const uint8_t*>(a->v.ptr);
   p.k_sb = a->k.stride_b * ek; p.k_ss = a->k.stride_s * ek; p.k_sh = a->k.stride_h * ek;

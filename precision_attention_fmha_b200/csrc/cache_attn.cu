@@ -990,10 +990,10 @@ __global__ void __launch_bounds__(256) parts_merge_kernel(const __grid_constant_
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const bool live = k0 + k < n;
-      lse[k] = live ? __ldg(p.part_lse + (k0 + k) * rows + lse_at) : -INFINITY;
+      lse[k] = live ? p.part_lse[(k0 + k) * rows + lse_at] : -INFINITY;  // plain loads: written while this grid may already run
       const float4* src = reinterpret_cast<const float4*>(p.part_o + ((k0 + k) * rows + row) * 128 + l16 * 8);
-      v[k][0] = live ? __ldg(src) : make_float4(0.f, 0.f, 0.f, 0.f);
-      v[k][1] = live ? __ldg(src + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[k][0] = live ? src[0] : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[k][1] = live ? src[1] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     float mn = m;
 #pragma unroll
