@@ -219,7 +219,7 @@ WeightRuns weight_runs(const fmha_cache_args* a, int capacity, int n_weights, in
   const int64_t keys = ceil_div(std::min(capacity, n_weights), 128);
   int64_t total = static_cast<int64_t>(a->B) * a->Hkv * keys * most;
   if (causal && capacity <= 2 * static_cast<int64_t>(a->T)) total /= 2;
-  const int64_t chunk = std::min(most, std::max<int64_t>(8, total / (16 * sm_count())));
+  const int64_t chunk = std::min(most, std::max<int64_t>(8, total / (8 * sm_count())));
   return {static_cast<int>(chunk), static_cast<int>((most + chunk - 1) / chunk)};
 }
 

@@ -252,19 +252,53 @@ __global__ void __launch_bounds__(KmCfg<D>::THREADS, 2)
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&misc->q_full[i]), 1);
       mbar_init(smem_addr(&misc->q_empty[i]), 1);
-      mbar_init(smem_addr(&misc->s_full[i]), 1);
+      mbar_init(smem_addr(&misc->s_full[i]), 2);  // the product, and the log-sum-exps that the MMA warp has seen arrive
       mbar_init(smem_addr(&misc->s_free[i]), C::SUM_THREADS / 32);
     }
     for (int i = 0; i < 8; ++i) mbar_init(smem_addr(&misc->nl_full[i]), 32);
     mbar_init(smem_addr(&misc->drain), 1);
     misc->abort = 0u;
-    misc->item[0] = atomicAdd(p.ticket, 1u);
     fence_barrier_init();
   }
   if (warp == C::MMA_WARP) {
     tmem_alloc(smem_addr(&misc->tmem_base), C::TMEM_COLS);
     tmem_relinquish();
   }
+  // An item's keys, queries and run.
+  struct Item {
+    int part, kt, bh, b, hkv, key0, n_keys, base, tt0, it0, n_it;
+    SeqLens s;
+  };
+  auto decode = [&](uint32_t item) {
+    Item x;
+    x.part = item % p.parts;
+    const int tile = item / p.parts;
+    x.kt = tile / bh_n;
+    x.bh = tile - x.kt * bh_n;
+    x.b = x.bh / p.c.Hkv;
+    x.hkv = x.bh - x.b * p.c.Hkv;
+    bool bad;
+    x.s = seq_lens(p.c, x.b, bad);
+    if (x.kt == 0 && x.hkv == 0 && x.part == 0 && (bad || x.s.len > p.n_weights)) atomicOr(p.c.err, kErrLength);
+    x.key0 = x.kt * 128;
+    x.n_keys = min(128, min(x.s.len, p.n_weights) - x.key0);
+    x.base = x.s.len - x.s.q;  // position of token 0
+    x.tt0 = p.causal ? max(0, x.key0 - x.base) / 128 : 0;
+    const int n_tt = max(0, (x.s.q + 127) / 128 - x.tt0);
+    x.it0 = x.part * p.chunk;  // this run's tiles: it0 + [0, n_it) of n_tt * G
+    x.n_it = min(p.chunk, n_tt * p.c.G - x.it0);
+    return x;
+  };
+  // The next item with work, drawn by one thread (the first run of a key tile writes its zeros even without queries).
+  auto draw = [&]() {
+    for (;;) {
+      const uint32_t item = atomicAdd(p.ticket, 1u);
+      if (item >= p.n_items) return item;
+      const Item x = decode(item);
+      if (x.n_keys > 0 && (x.n_it > 0 || x.part == 0)) return item;
+    }
+  };
+  if (tid == 0) misc->item[0] = draw();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -278,24 +312,10 @@ __global__ void __launch_bounds__(KmCfg<D>::THREADS, 2)
     // Items in order: the first keys are seen by the most queries and start first.
     const uint32_t item = misc->item[turn & 1];
     if (item >= p.n_items || misc->abort) break;
-    const int part = item % p.parts, tile = item / p.parts;
-    const int kt = tile / bh_n, bh = tile - kt * bh_n;
-    const int b = bh / p.c.Hkv, hkv = bh - b * p.c.Hkv;
-    if (warp == C::LOAD_WARP && lane == 0) misc->item[(turn + 1) & 1] = atomicAdd(p.ticket, 1u);
-    bool bad;
-    const SeqLens s = seq_lens(p.c, b, bad);
-    if (kt == 0 && hkv == 0 && part == 0 && tid == 0 && (bad || s.len > p.n_weights)) atomicOr(p.c.err, kErrLength);
-    const int key0 = kt * 128;
-    const int n_keys = min(128, min(s.len, p.n_weights) - key0);
-    const int base = s.len - s.q;  // position of token 0
-    const int tt0 = p.causal ? max(0, key0 - base) / 128 : 0;
-    const int n_tt = max(0, (s.q + 127) / 128 - tt0);
-    const int it0 = part * p.chunk;  // this run's tiles: it0 + [0, n_it) of n_tt * G
-    const int n_it = min(p.chunk, n_tt * p.c.G - it0);
-    if (n_keys <= 0 || (n_it <= 0 && part > 0)) {
-      __syncthreads();  // the next item is there
-      continue;
-    }
+    const Item x = decode(item);
+    const int part = x.part, bh = x.bh, b = x.b, hkv = x.hkv, key0 = x.key0, n_keys = x.n_keys, base = x.base, tt0 = x.tt0;
+    const int it0 = x.it0, n_it = x.n_it;
+    const SeqLens s = x.s;
     // Query tile `it`: the copy, and the log-sum-exps of its 128 tokens (four per lane, one tile ahead in registers).
     float lse4[4];
     auto fetch_lse = [&](int it) {
@@ -360,6 +380,7 @@ __global__ void __launch_bounds__(KmCfg<D>::THREADS, 2)
 
     if (warp == C::LOAD_WARP) {  // query tiles
       for (; sent < n_it && ok; sent += ok) ok = send_query(sent);
+      if (lane == 0) misc->item[(turn + 1) & 1] = draw();  // while the last tiles are summed
     } else if (warp == C::MMA_WARP) {  // S^T = K Q^T
       auto lo = [](uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | (1u << 16); };
       const uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
@@ -368,6 +389,7 @@ __global__ void __launch_bounds__(KmCfg<D>::THREADS, 2)
         const int n = cnt + it, st = n & 1;
         const uint32_t ph = (n >> 1) & 1;
         if (!__all_sync(kFull, w.wait(smem_addr(&misc->q_full[st]), ph)) ||
+            !__all_sync(kFull, w.wait(smem_addr(&misc->nl_full[n & 7]), (n >> 3) & 1)) ||
             !__all_sync(kFull, w.wait(smem_addr(&misc->s_free[st]), ph ^ 1)))
           break;
         tc_fence_after();
@@ -379,6 +401,7 @@ __global__ void __launch_bounds__(KmCfg<D>::THREADS, 2)
             if (i == 0) mma_ss_f16_lean<false>(tmem + st * 128, k_lo + off, hi, q, hi, C::IDESC);
             else mma_ss_f16_lean<true>(tmem + st * 128, k_lo + off, hi, q, hi, C::IDESC);
           }
+          mbar_arrive(smem_addr(&misc->s_full[st]));
           tc_commit(smem_addr(&misc->s_full[st]));
           tc_commit(smem_addr(&misc->q_empty[st]));
         }
@@ -391,8 +414,7 @@ __global__ void __launch_bounds__(KmCfg<D>::THREADS, 2)
       double total = 0.0;  // 32 bits inside a tile, 64 across: a prompt's sum has tens of thousands of terms
       for (int it = 0; it < n_it; ++it) {
         const int n = cnt + it, st = n & 1;
-        ok = __all_sync(kFull, w.wait(smem_addr(&misc->s_full[st]), (n >> 1) & 1)) &&
-             __all_sync(kFull, w.wait(smem_addr(&misc->nl_full[n & 7]), (n >> 3) & 1));
+        ok = __all_sync(kFull, w.wait(smem_addr(&misc->s_full[st]), (n >> 1) & 1));
         if (!ok) break;
         tc_fence_after();
         const int t0 = (tt0 + (it0 + it) / p.c.G) * 128 + side * 64;
