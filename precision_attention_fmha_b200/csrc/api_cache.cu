@@ -547,7 +547,7 @@ fmha_status fmha_key_weights(const fmha_cache_args* a, float* weights, int32_t n
     p.row_tiles = 1;
     p.min_tiles = 1;
     const int64_t tiles = heads * ceil_div(p.c.capacity, kTile);
-    p.n_ctas = static_cast<int>(std::min<int64_t>(2 * sm_count(), tiles));
+    p.n_ctas = static_cast<int>(std::min<int64_t>(3 * sm_count(), tiles));
     if (tiles / p.n_ctas >= (int64_t(1) << 30)) return fail(FMHA_ERR_UNSUPPORTED, "grid too large");
     e = launch_key_weights_few(a->D, k8, p, m, stream);
   }

@@ -120,6 +120,15 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t x) {
   return (x & E) + ONE;
 }
 
+// Scores of 16 queries x 16 keys, 32 columns (k-steps 2 s and 2 s + 1), from a fragment load of K's codes.
+template <int KS>
+__device__ __forceinline__ void mma_k8(float (&s0)[4], float (&s1)[4], const uint32_t (&qf)[KS][4], int s,
+                                       const uint32_t (&r)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e)  // e: which 16 columns (bit 0), which 8 keys (bit 1)
+    ptx::mma_f16(e & 2 ? s1 : s0, qf[2 * s + (e & 1)], ptx::e4m3x2_to_f16x2(r[e] & 0xffffu), ptx::e4m3x2_to_f16x2(r[e] >> 16));
+}
+
 template <class C>
 __device__ void consume(const CacheAttnParams& p, uint8_t* ring, float* red, CaMisc<C::STAGES>* misc, const Waiter w) {
   using namespace ptx;
@@ -508,26 +517,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
-}
-
-// K fragments as the 16-row side (16 keys): k-steps 2 s and 2 s + 1 (E4M3), or s (BF16).
-template <class C>
-__device__ __forceinline__ void load_kt(uint32_t (&a)[C::K8 ? 2 : 1][4], uint32_t k_base, int key0, int s, int lane) {
-  using namespace ptx;
-  uint32_t r[4];
-  ldsm4(r, k_base + C::KL::at(key0 + (lane & 15), 2 * s + (lane >> 4)));
-  if constexpr (C::K8) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      a[h][0] = e4m3x2_to_f16x2(r[2 * h] & 0xffffu);
-      a[h][1] = e4m3x2_to_f16x2(r[2 * h + 1] & 0xffffu);
-      a[h][2] = e4m3x2_to_f16x2(r[2 * h] >> 16);
-      a[h][3] = e4m3x2_to_f16x2(r[2 * h + 1] >> 16);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) a[0][i] = r[i];
-  }
 }
 
 // V^T fragments of columns 32 q .. 32 q + 31 (two 16-row tiles) x 16 keys.

@@ -19,6 +19,9 @@ __device__ __forceinline__ float neg_lse2(float lse) {  // -lse in log2 units; a
 }
 
 // ---- few query rows: a 64-key ring, four warps of 16 keys each (K bytes bound it) ----
+// S^T = K Q^T with the keys on the 16-row side, 8 query rows at a time: a
+// thread's scores are two keys' (gq, gq + 8), so the sum over rows crosses only
+// the four lanes of a key.
 template <int D_, bool K8_>
 struct KwCfg {
   static constexpr int D = D_, MODE = WALK_KEYS;
@@ -26,7 +29,7 @@ struct KwCfg {
   using KL = TileLayout<D, K8>;
   using VL = KL;
   static constexpr int SLOT = KL::BYTES;
-  static constexpr int STAGES = 6;
+  static constexpr int STAGES = 65536 / SLOT > 8 ? 8 : 65536 / SLOT;
   static constexpr int SMEM = STAGES * SLOT + 2048;
   static constexpr int THREADS = 160;
 };
@@ -34,7 +37,7 @@ struct KwCfg {
 template <class C>
 __device__ void weigh(const KeyWeightsParams& p, uint8_t* ring, RingMisc<C::STAGES>* misc, const Waiter w) {
   using namespace ptx;
-  constexpr int D = C::D, KS = D / 16;
+  constexpr int D = C::D, KS = D / 16, KF = C::K8 ? KS / 2 : KS;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gq = lane >> 2, j = lane & 3;
   uint32_t it = 0;
@@ -42,98 +45,93 @@ __device__ void weigh(const KeyWeightsParams& p, uint8_t* ring, RingMisc<C::STAG
   Walk<C::MODE> walk;
   walk.start(p);
   Seg g;
-  const int rows = p.c.T * p.c.G, tiles = (rows + 15) / 16;
+  const int rows = p.c.T * p.c.G, tiles = (rows + 7) / 8;
   while (ok && walk.next(p, g)) {
     const int64_t bh = g.b * static_cast<int64_t>(p.c.Hkv) + g.hkv;
     if (g.limit > p.n_weights && threadIdx.x == 0) atomicOr(p.c.err, kErrLength);
     const float c0 = p.scale_log2 * sf_of(p.sf_k, p.sf_k_kind, bh);
-    uint32_t qf[KS][4];
+    uint32_t qf[KS][2];
     float nl[2], cs[2];
-    int at[2];  // position of the rows' tokens
+    int at[2];  // position of the tokens of rows 2 j and 2 j + 1
     auto load_rows = [&](int rt) {
+      const int r = rt * 8 + gq;
+      const int t = r / p.c.G;
+      const int head = g.hkv * p.c.G + r - t * p.c.G;
+      const bool live = t < g.nodes;  // token rows in use (r < rows follows: nodes <= T)
+      const float x = live ? neg_lse2(__ldg(p.lse + (static_cast<int64_t>(g.b) * p.c.Hq + head) * p.c.T + t)) : -INFINITY;
+      float f;
+      load_q<C::K8, KS, 2>(qf, 0, f, p.q + g.b * p.q_sb + static_cast<int64_t>(t) * p.q_ss + head * p.q_sh, live, j);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = rt * 16 + gq + 8 * h;
-        const int t = r / p.c.G;
-        const int head = g.hkv * p.c.G + r - t * p.c.G;
-        const bool live = t < g.nodes;  // token rows in use (r < rows follows: nodes <= T)
-        at[h] = g.ctx - g.nodes + t;
-        nl[h] = live ? neg_lse2(__ldg(p.lse + (static_cast<int64_t>(g.b) * p.c.Hq + head) * p.c.T + t)) : -INFINITY;
-        load_q<C::K8, KS, 4>(qf, h, cs[h], p.q + g.b * p.q_sb + static_cast<int64_t>(t) * p.q_ss + head * p.q_sh, live, j);
-        cs[h] *= c0;
+      for (int e = 0; e < 2; ++e) {
+        nl[e] = __shfl_sync(kFull, x, 4 * (2 * j + e));
+        cs[e] = c0 * __shfl_sync(kFull, f, 4 * (2 * j + e));
+        at[e] = g.ctx - g.nodes + __shfl_sync(kFull, t, 4 * (2 * j + e));
       }
     };
     if (tiles == 1) load_rows(0);
-    // Lanes of the first row group hold the sums of keys 2 j, 2 j + 1, 2 j + 8, 2 j + 9; what the weights held is
-    // fetched one tile ahead (the load's latency in every tile was two thirds of a decoding step's time).
-    auto fetch = [&](int u, float (&x)[4]) {
+    // The first lane of a key writes its sum; what the weights held is fetched one tile ahead (the load's latency in every
+    // tile was two thirds of a decoding step's time).
+    auto fetch = [&](int u, float (&x)[2]) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int key = u * kTileKeys + warp * 16 + 8 * (e >> 1) + 2 * j + (e & 1);
-        x[e] = p.accumulate && gq == 0 && u < g.t1 && key < min(g.limit, p.n_weights) ? p.weights[bh * p.n_weights + key] : 0.f;
+      for (int e = 0; e < 2; ++e) {
+        const int key = u * kTileKeys + warp * 16 + gq + 8 * e;
+        x[e] = p.accumulate && j == 0 && u < g.t1 && key < min(g.limit, p.n_weights) ? p.weights[bh * p.n_weights + key] : 0.f;
       }
     };
-    float old[4], ahead[4];
+    float old[2], ahead[2];
     fetch(g.t0, ahead);
     for (int u = g.t0; u < g.t1; ++u) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) old[e] = ahead[e];
+      for (int e = 0; e < 2; ++e) old[e] = ahead[e];
       fetch(u + 1, ahead);
       const int s = it % C::STAGES;
       ok = __all_sync(kFull, w.wait(smem_addr(&misc->full[s]), (it / C::STAGES) & 1));
       if (!ok) break;
       ++it;
-      const uint32_t k_base = smem_addr(ring + s * C::SLOT);
       const int valid = misc->meta[s].valid[warp], pos = misc->meta[s].pos[warp];
-      uint32_t kb[C::K8 ? KS / 2 : KS][4];  // the warp's 16 keys
+      uint32_t kf[KF][C::K8 ? 2 : 1][4];  // the warp's 16 keys
       if (valid > 0) {
-        const int row = warp * 16 + (lane & 7) + (lane >> 4) * 8;
 #pragma unroll
-        for (int i = 0; i < (C::K8 ? KS / 2 : KS); ++i) ldsm4(kb[i], k_base + C::KL::at(row, 2 * i + ((lane >> 3) & 1)));
+        for (int i = 0; i < KF; ++i) load_kt<C>(kf[i], smem_addr(ring + s * C::SLOT), warp * 16, i, lane);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&misc->empty[s]));
       if (valid <= 0) continue;
-      float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+      float sum[2] = {0.f, 0.f};
       for (int rt = 0; rt < tiles; ++rt) {
         if (tiles > 1) load_rows(rt);
-        float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};  // two chains
 #pragma unroll
-        for (int i = 0; i < KS; ++i) {
+        for (int i = 0; i < KF; ++i) {
           if constexpr (C::K8) {
-            if (i % 2 == 0) mma_k8<KS>(sc[0], sc[1], qf, i / 2, kb[i / 2]);
+            mma_f16(sc[0], kf[i][0], qf[2 * i][0], qf[2 * i][1]);
+            mma_f16(sc[1], kf[i][1], qf[2 * i + 1][0], qf[2 * i + 1][1]);
           } else {
-            mma_bf16(sc[0], qf[i], kb[i][0], kb[i][1]);
-            mma_bf16(sc[1], qf[i], kb[i][2], kb[i][3]);
+            mma_bf16(sc[i & 1], kf[i][0], qf[i][0], qf[i][1]);
           }
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int key = pos + 8 * i + 2 * j + (e & 1);
-            const float x = ex2(fmaf(sc[i][e], cs[e >> 1], nl[e >> 1]));
-            // hidden: later than the row's token (a key past the end holds anything, and is not written below)
-            sum[i][e & 1] += (p.causal && key > at[e >> 1]) || nl[e >> 1] == -INFINITY ? 0.f : x;
-          }
+        for (int e = 0; e < 4; ++e) {  // key gq + 8 (e >> 1), row 2 j + (e & 1)
+          const int key = pos + gq + 8 * (e >> 1);
+          const float x = ex2(fmaf(sc[0][e] + sc[1][e], cs[e & 1], nl[e & 1]));
+          // hidden: later than the row's token (a key past the end holds anything, and is not written below)
+          sum[e >> 1] += (p.causal && key > at[e & 1]) || nl[e & 1] == -INFINITY ? 0.f : x;
+        }
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float v = sum[i][e];
-          v += __shfl_xor_sync(kFull, v, 4);
-          v += __shfl_xor_sync(kFull, v, 8);
-          v += __shfl_xor_sync(kFull, v, 16);
-          const int k = 8 * i + 2 * j + e;
-          if (gq == 0 && k < valid && pos + k < p.n_weights) p.weights[bh * p.n_weights + pos + k] = old[2 * i + e] + v;
-        }
+      for (int e = 0; e < 2; ++e) {
+        float v = sum[e];
+        v += __shfl_xor_sync(kFull, v, 1);
+        v += __shfl_xor_sync(kFull, v, 2);
+        const int k = gq + 8 * e;
+        if (j == 0 && k < valid && pos + k < p.n_weights) p.weights[bh * p.n_weights + pos + k] = old[e] + v;
+      }
     }
   }
 }
 
 template <class C>
-__global__ void __launch_bounds__(C::THREADS, 2)
+__global__ void __launch_bounds__(C::THREADS, 3)
     key_weights_few_kernel(const __grid_constant__ KeyWeightsParams p, const __grid_constant__ CUtensorMap tk) {
   using namespace ptx;
   extern __shared__ uint8_t smem_raw[];
