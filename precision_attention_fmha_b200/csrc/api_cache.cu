@@ -112,14 +112,14 @@ fmha_status cache_map(CUtensorMap* m, const fmha_cache_args* a, const CacheView&
 
 constexpr int kPackedRows = 64;       // packed rows (T * G), and
 constexpr int kPackedKeys = 1024;     // keys of room, from which the context goes to the packed kernel
-constexpr int kPackedCtasPerSm = 2;
+constexpr int kPackedCtasPerSm = 1;
 
 // The sizes of an attention call that do not need the device: grid and row
 // tiles of the tree form.
 struct TreePlan {
   int rows, row_tiles, n_ctas;
   // The context's whole 128-key tiles on the decode path's packed kernel: query-tile units of a KV head, KV splits and
-  // partial outputs (the last one is the tail's). 0 parts: the few-row kernel takes everything.
+  // partial outputs, which the few-row kernel joins with what it takes itself. 0 parts: it takes everything.
   int units, n_splits, interleave, n_parts;
   size_t workspace_bytes;
 };
@@ -152,7 +152,7 @@ bool tree_plan(const fmha_cache_args* a, int capacity, TreePlan* t) {
     // A few CTAs per SM even out the sequences' lengths; a split keeps at least 8 tiles.
     const int64_t want = (kPackedCtasPerSm * sm_count() + base - 1) / base;
     t->n_splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(want, kv / 8)));
-    t->n_parts = t->n_splits * (t->interleave ? 2 : 1) + 1;
+    t->n_parts = t->n_splits * (t->interleave ? 2 : 1);
     t->n_ctas = static_cast<int>(std::min<int64_t>(2 * sm_count(), items));
     t->workspace_bytes = size_t(t->n_parts) * a->B * a->T * a->Hq * (size_t(a->D) + 1) * 4;
     if (base * t->n_splits >= (int64_t(1) << 31) || static_cast<int64_t>(a->B) * a->T * a->Hq >= (int64_t(1) << 32)) return false;
@@ -292,7 +292,7 @@ fmha_status packed_params(const fmha_cache_args* a, const CacheAttnParams& c, co
   p->n_splits = t.n_splits;
   p->split_tiles = ceil_div(p->n_kv_blocks, t.n_splits);
   p->kv_interleave = t.interleave;
-  p->n_parts = t.n_parts;  // at least two: every tile writes a partial
+  p->n_parts = t.n_parts + 1;  // more than one: every tile writes a partial, which the tail joins
   p->ctx_lens = c.c.lens;
   p->q_lens = c.c.q_lens;
   p->o_part = c.part_o;
@@ -347,13 +347,12 @@ fmha_status fmha_fwd_tree(const fmha_cache_args* a, const uint8_t* tree_mask, in
   cudaError_t e;
   if (t.n_parts > 0) {
     p.part_lse = p.part_o + size_t(t.n_parts) * a->B * a->T * a->Hq * a->D;
-    p.tail_part = t.n_parts - 1;
+    p.n_parts = t.n_parts;
     AttnParams ap;
     CUtensorMap tq, tkp, tvp;
     if ((st = packed_params(a, p, t, &ap, &tq, &tkp, &tvp)) != FMHA_OK) return st;
     e = launch_attention_packed(QK_BF16, PV_BF16, p.c.page_table != nullptr, ap, tq, tkp, tvp, tq, stream);
     if (e == cudaSuccess) e = launch_cache_tail(p, tk, tv, stream);
-    if (e == cudaSuccess) e = launch_parts_merge(p, stream);
   } else {
     p.part_lse = p.part_o + size_t(2) * t.n_ctas * t.rows * a->D;
     e = launch_cache_attn(a->D, k8, v8, p, tk, tv, stream);

@@ -379,6 +379,7 @@ __device__ void consume(const CacheAttnParams& p, uint8_t* ring, float* red, CaM
     const bool whole = g.t0 == 0 && g.t1 == g.nt;
     const int64_t slot = 2ll * blockIdx.x + (g.t0 == 0 ? 1 : 0);
     if constexpr (C::WN == 1) {
+      if constexpr (C::TAIL) asm volatile("griddepcontrol.wait;" ::: "memory");  // the packed kernel's parts are there
       // A warp has its rows to itself and writes them from its registers, 16 bytes and more of a row at a time.
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -387,10 +388,9 @@ __device__ void consume(const CacheAttnParams& p, uint8_t* ring, float* red, CaM
         const bool mine = ro.tok >= 0 && ok;
         float M, L;
         total(wm, gq + 8 * h, M, L);
-        const float lse = L != 0.f ? M + __log2f(L) : -INFINITY;
-        if (C::TAIL || !whole) {
-          const int64_t at = C::TAIL ? ((static_cast<int64_t>(p.tail_part) * p.c.B + g.b) * p.c.T + ro.tok) * p.c.Hq + ro.head
-                                     : slot * C::ROWS + item_row;
+        float lse = L != 0.f ? M + __log2f(L) : -INFINITY;
+        if (!C::TAIL && !whole) {
+          const int64_t at = slot * C::ROWS + item_row;
           float* dst = p.part_o + at * D;
 #pragma unroll
           for (int q = 0; q < NQ; ++q) {
@@ -409,13 +409,38 @@ __device__ void consume(const CacheAttnParams& p, uint8_t* ring, float* red, CaM
                       make_float2(acc[4 * q + n][2 * h] * f[h], acc[4 * q + n][2 * h + 1] * f[h]);
             }
           }
-          if (mine && j == 0) {
-            if constexpr (C::TAIL)
-              p.part_lse[((static_cast<int64_t>(p.tail_part) * p.c.B + g.b) * p.c.Hq + ro.head) * p.c.T + ro.tok] =
-                  lse * 0.69314718055994531f;
-            else p.part_lse[at] = lse;
-          }
+          if (mine && j == 0) p.part_lse[at] = lse;
         } else {
+          if constexpr (C::TAIL) {
+            // Join the packed kernel's partial results of the context's whole 128-key tiles.
+            if (mine && ro.tok < g.nodes) {
+              const int64_t rows_n = static_cast<int64_t>(p.c.B) * p.c.T * p.c.Hq;
+              const int64_t at_o = (static_cast<int64_t>(g.b) * p.c.T + ro.tok) * p.c.Hq + ro.head;
+              const int64_t at_l = (static_cast<int64_t>(g.b) * p.c.Hq + ro.head) * p.c.T + ro.tok;
+              for (int k = 0; k < p.n_parts; ++k) {
+                const float x = p.part_lse[k * rows_n + at_l] * 1.4426950408889634f;
+                if (x == -INFINITY) continue;  // a part without keys
+                const float2* src = reinterpret_cast<const float2*>(p.part_o + (k * rows_n + at_o) * D) + j;
+                float2 v[NQ * 4];
+#pragma unroll
+                for (int n = 0; n < NQ * 4; ++n) v[n] = src[4 * n];
+                const float mn = fmaxf(M, x);
+                const float fo = M == -INFINITY ? 0.f : ex2(M - mn), fx = ex2(x - mn);
+                // acc f is O so far, of weight L 2^M (a NaN sum stays one)
+                const float wo = L * fo, sum = wo + fx;
+                const float ao = sum != 0.f ? f[h] * wo / sum : 0.f, ax = sum != 0.f ? fx / sum : 0.f;
+#pragma unroll
+                for (int n = 0; n < NQ * 4; ++n) {
+                  acc[n][2 * h] = fmaf(v[n].x, ax, L != 0.f ? acc[n][2 * h] * ao : 0.f);
+                  acc[n][2 * h + 1] = fmaf(v[n].y, ax, L != 0.f ? acc[n][2 * h + 1] * ao : 0.f);
+                }
+                f[h] = 1.f;
+                M = mn;
+                L = sum;
+              }
+              lse = L != 0.f ? M + __log2f(L) : -INFINITY;
+            }
+          }
           const bool hide = !C::PICKED && ro.tok >= g.nodes;  // a padding row: its factor may be anything
           uint16_t* dst = p.o + g.b * p.o_sb + ro.tok * p.o_ss + ro.head * p.o_sh;
           auto pair = [&](float x, float y) { return hide ? 0u : pack_bf16x2(x * f[h], y * f[h]); };
@@ -448,9 +473,7 @@ __device__ void consume(const CacheAttnParams& p, uint8_t* ring, float* red, CaM
       __syncwarp();  // the next item's (m, l) may be written
       continue;
     }
-    // Lanes that write: WN > 1: 8 per row over all 128 threads; else 8 per row of the warp.
-    const int tid = C::WN > 1 ? threadIdx.x : lane;
-    constexpr int PASS_ROWS = C::WN > 1 ? 16 : 4, PASSES = (C::WN > 1 ? C::ROWS : 16) / PASS_ROWS;
+    // Two warps share the rows: eight lanes write a row, 16 rows a pass.
 #pragma unroll 1
     for (int q = 0; q < NQ; ++q) {
       float* mine = red + warp * 16 * C::RED_LD;
@@ -465,12 +488,11 @@ __device__ void consume(const CacheAttnParams& p, uint8_t* ring, float* red, CaM
             if (qq == q) v = acc[4 * qq + n][e];
           mine[(gq + 8 * (e >> 1)) * C::RED_LD + col] = v * f[e >> 1];
         }
-      if (C::WN > 1) named_bar_sync(1, 128);
-      else __syncwarp();
+      named_bar_sync(1, 128);
 #pragma unroll
-      for (int ps = 0; ps < PASSES; ++ps) {
-        const int r = ps * PASS_ROWS + tid / 8, c4 = tid % 8;
-        const int wmi = C::WN > 1 ? r / 16 : wm, rr = r % 16;
+      for (int ps = 0; ps < C::ROWS / 16; ++ps) {
+        const int r = ps * 16 + threadIdx.x / 8, c4 = threadIdx.x % 8;
+        const int wmi = r / 16, rr = r % 16;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int x = 0; x < C::WN; ++x) {
@@ -481,24 +503,18 @@ __device__ void consume(const CacheAttnParams& p, uint8_t* ring, float* red, CaM
         const int item_row = wmi * 16 + rr;
         const Row ro = row_of<C>(p, g, item_row);
         if (ro.tok < 0 || !ok) continue;
-        if constexpr (C::TAIL) {  // one partial of the row, in the layout of the packed kernel's
-          const int64_t at = ((static_cast<int64_t>(p.tail_part) * p.c.B + g.b) * p.c.T + ro.tok) * p.c.Hq + ro.head;
-          *reinterpret_cast<float4*>(p.part_o + at * D + 32 * q + 4 * c4) = v;
-        } else if (!whole) {
+        if (!whole) {
           *reinterpret_cast<float4*>(p.part_o + (slot * C::ROWS + item_row) * D + 32 * q + 4 * c4) = v;
         } else {
           if (!C::PICKED && ro.tok >= g.nodes) v = make_float4(0.f, 0.f, 0.f, 0.f);
           uint16_t* dst = p.o + g.b * p.o_sb + ro.tok * p.o_ss + ro.head * p.o_sh + 32 * q + 4 * c4;
           *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
         }
-        if (q == 0 && c4 == 0 && (C::TAIL || !whole || p.lse != nullptr)) {
+        if (q == 0 && c4 == 0 && (!whole || p.lse != nullptr)) {
           float M, L;
           total(wmi, rr, M, L);
           float lse = L != 0.f ? M + __log2f(L) : -INFINITY;
-          if constexpr (C::TAIL) {
-            p.part_lse[((static_cast<int64_t>(p.tail_part) * p.c.B + g.b) * p.c.Hq + ro.head) * p.c.T + ro.tok] =
-                lse * 0.69314718055994531f;
-          } else if (!whole) {
+          if (!whole) {
             p.part_lse[slot * C::ROWS + item_row] = lse;
           } else {
             if (!C::PICKED && ro.tok >= g.nodes) lse = -INFINITY;
@@ -506,8 +522,7 @@ __device__ void consume(const CacheAttnParams& p, uint8_t* ring, float* red, CaM
           }
         }
       }
-      if (C::WN > 1) named_bar_sync(1, 128);
-      else __syncwarp();
+      named_bar_sync(1, 128);
     }
   }
 }
@@ -840,7 +855,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     cache_attn_kernel(const __grid_constant__ CacheAttnParams p, const __grid_constant__ CUtensorMap tk,
                       const __grid_constant__ CUtensorMap tv) {
   using namespace ptx;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if constexpr (!C::TAIL) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* red = reinterpret_cast<float*>(ring + C::STAGES * C::SLOT);
@@ -860,8 +875,6 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   else if constexpr (C::NT > 0) consume_t<C>(p, ring, red, misc, w);
   else consume<C>(p, ring, red, misc, w);
   __syncthreads();
-  // The merge that follows waits for this grid alone: let it end after the packed kernel's.
-  if constexpr (C::TAIL) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Merges the partials of items that several CTAs shared, and writes the rows
@@ -954,62 +967,6 @@ __global__ void __launch_bounds__(128) cache_merge_kernel(const __grid_constant_
     *lse_out = sum != 0.f ? (mx + __log2f(sum)) * 0.69314718055994531f : -INFINITY;
 }
 
-// Joins the parts of a packed call's rows (D = 128). Two rows per warp, 16 lanes
-// of 8 columns each; a row's parts are loaded before their weights are known,
-// so a row costs one memory latency (65536 rows of 3 parts: 73 us with the
-// weights first, 30 us so).
-__global__ void __launch_bounds__(256) parts_merge_kernel(const __grid_constant__ CacheAttnParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int half = (threadIdx.x >> 4) & 1, l16 = threadIdx.x & 15;
-  const long long rows = static_cast<long long>(p.c.B) * p.c.T * p.c.Hq;
-  const long long row = (static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * 2 + half;
-  if (row >= rows) return;
-  const int h = static_cast<int>(row % p.c.Hq);
-  const long long bt = row / p.c.Hq;
-  const int tok = static_cast<int>(bt % p.c.T), b = static_cast<int>(bt / p.c.T);
-  const int n = p.tail_part + 1;
-  const long long lse_at = (static_cast<long long>(b) * p.c.Hq + h) * p.c.T + tok;
-  bool bad;
-  const bool hidden = tok >= tree_lens(p.c, b, bad).q;
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  float m = -INFINITY, sum = 0.f;
-  for (int k0 = 0; k0 < n && !hidden; k0 += 4) {
-    float lse[4];
-    float4 v[4][2];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const bool live = k0 + k < n;
-      lse[k] = live ? p.part_lse[(k0 + k) * rows + lse_at] : -INFINITY;  // plain loads: written while this grid may already run
-      const float4* src = reinterpret_cast<const float4*>(p.part_o + ((k0 + k) * rows + row) * 128 + l16 * 8);
-      v[k][0] = live ? src[0] : make_float4(0.f, 0.f, 0.f, 0.f);
-      v[k][1] = live ? src[1] : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    float mn = m;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) mn = fmaxf(mn, lse[k]);
-    const float mb = mn == -INFINITY ? 0.f : mn;
-    const float f = m == mn ? 1.f : expf(m - mb);
-    m = mn;
-    sum *= f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] *= f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (lse[k] == -INFINITY) continue;  // a part that saw no key
-      const float w = expf(lse[k] - mb);
-      sum += w;
-      const float x[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w, v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, x[e], acc[e]);
-    }
-  }
-  const float inv = sum != 0.f ? 1.f / sum : 0.f;
-  *reinterpret_cast<uint4*>(p.o + b * p.o_sb + tok * p.o_ss + h * p.o_sh + l16 * 8) =
-      make_uint4(ptx::pack_bf16x2(acc[0] * inv, acc[1] * inv), ptx::pack_bf16x2(acc[2] * inv, acc[3] * inv),
-                 ptx::pack_bf16x2(acc[4] * inv, acc[5] * inv), ptx::pack_bf16x2(acc[6] * inv, acc[7] * inv));
-  if (p.lse != nullptr && l16 == 0) p.lse[lse_at] = sum != 0.f ? m + logf(sum) : -INFINITY;
-}
-
 template <class C>
 cudaError_t launch_cfg(const CacheAttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
   auto kern = cache_attn_kernel<C>;
@@ -1052,7 +1009,7 @@ cudaError_t launch_cache_tail(const CacheAttnParams& p, const CUtensorMap& tk, c
   auto kern = cache_attn_kernel<C>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  // Starts on the SMs that the packed kernel's last CTAs leave free.
+  // Starts on the SMs that the packed kernel's last CTAs leave free, and waits for its end only to join its results.
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.n_ctas);
   cfg.blockDim = dim3(C::THREADS);
@@ -1085,20 +1042,6 @@ cudaError_t launch_cache_merge(int D, const CacheAttnParams& p, cudaStream_t s) 
                    : cudaLaunchKernelEx(&cfg, cache_merge_kernel<128, true>, p, rows);
   return D == 64 ? cudaLaunchKernelEx(&cfg, cache_merge_kernel<64, false>, p, rows)
                  : cudaLaunchKernelEx(&cfg, cache_merge_kernel<128, false>, p, rows);
-}
-
-cudaError_t launch_parts_merge(const CacheAttnParams& p, cudaStream_t s) {
-  const long long rows = static_cast<long long>(p.c.B) * p.c.T * p.c.Hq;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + 15) / 16));
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, parts_merge_kernel, p);
 }
 
 }  // namespace fmha

@@ -42,8 +42,8 @@ struct CacheAttnParams : CacheParams {
   const uint8_t* mask; int64_t mask_sb;
   float* part_o;    // [2 * n_ctas][rows per tile][D]
   float* part_lse;  // [2 * n_ctas][rows per tile], log2 units
-  // tail of a packed call: parts as the packed kernel writes them ([part][B, T, Hq, D] and [part][B, Hq, T]), its own index
-  int32_t tail_part;
+  // tail of a packed call: its parts ([n_parts][B, T, Hq, D], and [n_parts][B, Hq, T] in part_lse, natural log)
+  int32_t n_parts;
 };
 
 // Rows (query token x head of the group) that one CTA takes at once.
@@ -54,8 +54,6 @@ constexpr int cache_attn_ctas(int rows) { return rows <= 8 ? 3 : 2; }
 cudaError_t launch_cache_attn(int D, bool k8, bool v8, const CacheAttnParams& p, const CUtensorMap& tk,
                               const CUtensorMap& tv, cudaStream_t stream);
 cudaError_t launch_cache_tail(const CacheAttnParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream);
-// D = 128: joins the tail_part + 1 parts of each row.
-cudaError_t launch_parts_merge(const CacheAttnParams& p, cudaStream_t stream);
 cudaError_t launch_cache_merge(int D, const CacheAttnParams& p, cudaStream_t stream);
 
 // Attention weight that each cached key gathers over the query tokens.
