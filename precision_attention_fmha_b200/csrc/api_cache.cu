@@ -117,13 +117,26 @@ constexpr int kPackedCtasPerSm = 1;
 // The sizes of an attention call that do not need the device: grid and row
 // tiles of the tree form.
 struct TreePlan {
-  int rows, row_tiles, n_ctas;
+  int rows, row_tiles, n_ctas, groups;
   // The context's whole 128-key tiles on the decode path's packed kernel: query-tile units of a KV head, KV splits and
   // partial outputs, which the few-row kernel joins with what it takes itself. 0 parts: it takes everything.
   int units, n_splits, interleave, n_parts;
   size_t workspace_bytes;
 };
-constexpr int kMinTiles = 2;  // least key tiles of a CTA
+constexpr int kMinTiles = 2;  // least key tiles of a group
+
+// Groups of `heads` CTAs (one per KV head and row tile) that share the list of key tiles: as many as are resident at once,
+// or, where that leaves a thin last wave, the number with the least waves times work per CTA. At most `most` have work.
+int list_groups(int64_t heads, int64_t resident, int64_t most) {
+  int64_t best = 1;
+  double least = 1e30;
+  const int64_t limit = std::max<int64_t>(1, std::min(most, heads >= resident ? int64_t(4) : resident / heads));
+  for (int64_t g = heads >= resident ? 1 : limit; g <= limit; ++g) {
+    const double cost = static_cast<double>((heads * g + resident - 1) / resident) / static_cast<double>(g);
+    if (cost < least * 0.999) least = cost, best = g;
+  }
+  return static_cast<int>(best);
+}
 
 // Whether the context goes through 128-row tensor-memory tiles: many packed rows, and what that kernel is built for.
 bool tree_packed(const fmha_cache_args* a, int capacity) {
@@ -138,9 +151,11 @@ bool tree_plan(const fmha_cache_args* a, int capacity, TreePlan* t) {
   t->rows = cache_attn_rows(static_cast<int>(std::min<int64_t>(packed, 1 << 20)));
   t->row_tiles = static_cast<int>((packed + t->rows - 1) / t->rows);
   const int64_t items = static_cast<int64_t>(a->B) * a->Hkv * t->row_tiles;
-  const int64_t tiles = items * ceil_div(std::max(capacity, 1), kTile);
-  // More than one CTA per kMinTiles tiles has nothing to do.
-  t->n_ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(cache_attn_ctas(t->rows) * sm_count(), (tiles + kMinTiles - 1) / kMinTiles)));
+  const int64_t tiles = static_cast<int64_t>(a->B) * ceil_div(std::max(capacity, 1), kTile);
+  t->groups = list_groups(static_cast<int64_t>(a->Hkv) * t->row_tiles, cache_attn_ctas(t->rows) * sm_count(),
+                          (tiles + kMinTiles - 1) / kMinTiles);
+  if (static_cast<int64_t>(a->Hkv) * t->row_tiles * t->groups >= (int64_t(1) << 30)) return false;
+  t->n_ctas = a->Hkv * t->row_tiles * t->groups;
   t->workspace_bytes = size_t(2) * t->n_ctas * t->rows * (size_t(a->D) + 1) * 4;
   t->n_parts = 0;
   if (tree_packed(a, capacity)) {
@@ -157,7 +172,7 @@ bool tree_plan(const fmha_cache_args* a, int capacity, TreePlan* t) {
     t->workspace_bytes = size_t(t->n_parts) * a->B * a->T * a->Hq * (size_t(a->D) + 1) * 4;
     if (base * t->n_splits >= (int64_t(1) << 31) || static_cast<int64_t>(a->B) * a->T * a->Hq >= (int64_t(1) << 32)) return false;
   }
-  return items < (int64_t(1) << 31) && tiles / t->n_ctas < (int64_t(1) << 30);
+  return items < (int64_t(1) << 31) && tiles / t->groups < (int64_t(1) << 30);
 }
 
 struct PickPlan {
@@ -342,6 +357,7 @@ fmha_status fmha_fwd_tree(const fmha_cache_args* a, const uint8_t* tree_mask, in
   p.row_tiles = t.row_tiles;
   p.tile_rows = t.rows;
   p.n_ctas = t.n_ctas;
+  p.groups = t.groups;
   p.min_tiles = kMinTiles;
   p.part_o = static_cast<float*>(workspace);
   cudaError_t e;
@@ -545,9 +561,12 @@ fmha_status fmha_key_weights(const fmha_cache_args* a, float* weights, int32_t n
     p.piece_shift = log2_of(piece);
     p.row_tiles = 1;
     p.min_tiles = 1;
-    const int64_t tiles = heads * ceil_div(p.c.capacity, kTile);
-    p.n_ctas = static_cast<int>(std::min<int64_t>(3 * sm_count(), tiles));
-    if (tiles / p.n_ctas >= (int64_t(1) << 30)) return fail(FMHA_ERR_UNSUPPORTED, "grid too large");
+    if (heads >= (int64_t(1) << 30)) return fail(FMHA_ERR_UNSUPPORTED, "grid too large");
+    p.groups = list_groups(a->Hkv, 3 * sm_count(), static_cast<int64_t>(a->B) * ceil_div(p.c.capacity, kTile));
+    p.n_ctas = a->Hkv * p.groups;
+    if (static_cast<int64_t>(a->B) * ceil_div(p.c.capacity, kTile) / p.groups >= (int64_t(1) << 30) ||
+        static_cast<int64_t>(a->Hkv) * p.groups >= (int64_t(1) << 30))
+      return fail(FMHA_ERR_UNSUPPORTED, "grid too large");
     e = launch_key_weights_few(a->D, k8, p, m, stream);
   }
   if (e != cudaSuccess) return fail(FMHA_ERR_CUDA, "key weights launch: %s", cudaGetErrorString(e));

@@ -892,7 +892,7 @@ __global__ void __launch_bounds__(128) cache_merge_kernel(const __grid_constant_
   item /= p.c.Hkv;
   int tok, head, b;
   bool hidden = false;
-  long long first, last;  // CTAs that hold a partial of the item
+  long long first, last;  // CTAs (tree: groups of them) that hold a partial of the item
   if constexpr (PICKED) {
     tok = static_cast<int>(item % p.c.T);
     b = static_cast<int>(item / p.c.T);
@@ -912,8 +912,7 @@ __global__ void __launch_bounds__(128) cache_merge_kernel(const __grid_constant_
     const int nt = tiles_of<WALK_TREE>(s);
     hidden = tok >= s.q || nt == 0;
     const Share sh = list_share<WALK_TREE>(p, false);
-    const long long t0 = list_tiles<WALK_TREE>(p, b, false) * p.c.Hkv * p.row_tiles +
-                         static_cast<long long>(nt) * (hkv * p.row_tiles + rt);
+    const long long t0 = list_tiles<WALK_TREE>(p, b, false);
     first = t0 / sh.per;
     last = nt > 0 ? (t0 + nt - 1) / sh.per : first;
     if (nt > 0 && first == last) return;  // written whole
@@ -926,7 +925,10 @@ __global__ void __launch_bounds__(128) cache_merge_kernel(const __grid_constant_
   for (int i = 0; i < V; ++i) acc[i] = 0.f;
   float sum = 0.f, mx = -INFINITY;
   if (!hidden) {
-    auto slot = [&](long long c) { return (2 * c + (c == first ? 1 : 0)) * rows + row; };
+    auto slot = [&](long long c) {
+      const long long cta = PICKED ? c : c * p.c.Hkv * p.row_tiles + hkv * p.row_tiles + rt;
+      return (2 * cta + (c == first ? 1 : 0)) * rows + row;
+    };
     const int n = static_cast<int>(last - first + 1);
     for (int k = lane; k < n; k += 32) mx = fmaxf(mx, p.part_lse[slot(first + k)]);
 #pragma unroll

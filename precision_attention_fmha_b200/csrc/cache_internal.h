@@ -24,7 +24,8 @@ struct CacheParams {
   CacheView c;
   int32_t piece_shift;        // log2 of the rows of one TMA copy (16, 32 or 64)
   int32_t row_tiles, tile_rows;  // tiles of query rows per KV head, and rows of one
-  int32_t n_ctas, min_tiles;  // grid, and the least key tiles a CTA takes
+  int32_t n_ctas;             // grid
+  int32_t groups, min_tiles;  // groups of CTAs that share the list of key tiles, and the least tiles a group takes
   // picked blocks: [B, T, Hkv, top], a negative id is no block; key tiles of an item, and how CTAs share them
   const int32_t* blocks;
   int32_t top, block_shift, n_blocks;
