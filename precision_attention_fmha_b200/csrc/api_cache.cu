@@ -110,8 +110,12 @@ fmha_status cache_map(CUtensorMap* m, const fmha_cache_args* a, const CacheView&
                                   : row >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B);
 }
 
-constexpr int kPackedRows = 64;       // packed rows (T * G), and
-constexpr int kPackedKeys = 1024;     // keys of room, from which the context goes to the packed kernel
+// Which calls send their contexts to the packed kernel: from 128 packed rows (T * G) a whole tensor-memory tile; from 33
+// where (sequence, KV head) pairs give at least half the SMs a CTA. Few-row kernel against packed, 64 rows: 16 contexts of
+// 8-16k keys on 8 heads 283 against 163 us, 16 of 0.5-4k 79 against 69, 2 of 31k 106 against 118; 48 rows, 16 of 8-16k 282
+// against 160, 2 of 1.2k 19 against 25; 32 rows, 16 of 8-16k 150 against 158, 16 of 0.5-4k 50 against 64.
+constexpr int kPackedRows = 33, kPackedTile = 128;
+constexpr int kPackedKeys = 1024;  // keys of room; below, the packed kernel would mostly start and end
 constexpr int kPackedCtasPerSm = 1;
 
 // The sizes of an attention call that do not need the device: grid and row
@@ -143,7 +147,8 @@ bool tree_packed(const fmha_cache_args* a, int capacity) {
   const int G = a->Hq / a->Hkv;
   const int64_t rows = static_cast<int64_t>(a->T) * G;
   return a->D == 128 && a->k.dtype == FMHA_BF16 && a->v.dtype == FMHA_BF16 && (G & (G - 1)) == 0 && G <= 128 &&
-         rows >= kPackedRows && capacity >= kPackedKeys && capacity <= 131072;
+         (rows >= kPackedTile || (rows >= kPackedRows && 2 * static_cast<int64_t>(a->B) * a->Hkv >= sm_count())) &&
+         capacity >= kPackedKeys && capacity <= 131072;
 }
 
 bool tree_plan(const fmha_cache_args* a, int capacity, TreePlan* t) {

@@ -86,11 +86,12 @@ TREES = [
     (2, 1, 16, 1, 128, [2047, 90], 0, "e4m3"),
     (2, 6, 8, 4, 128, [100, 200], 32, "bf16_e4m3"),
     (2, 40, 4, 2, 64, [31, 257], 0, "bf16_e4m3"),
+    (24, 5, 64, 8, 128, [900 + 7 * i for i in range(24)], 64, "bf16"),  # 40 rows on many heads
     # many rows and room: contexts on the packed tensor-memory tiles, the rest joined
-    (2, 16, 32, 8, 128, [1500, 100], 64, "bf16"),
-    (3, 9, 64, 8, 128, [1023, 1024, 0], 16, "bf16"),   # 72 rows
+    (2, 16, 64, 8, 128, [1500, 100], 64, "bf16"),
+    (3, 17, 64, 8, 128, [1023, 1024, 0], 16, "bf16"),  # 136 rows
     (1, 40, 32, 4, 128, [2049], 0, "bf16"),            # 320 rows: three 128-row tiles
-    (2, 70, 4, 4, 128, [1279, 1408], 128, "bf16"),     # one head a group
+    (2, 140, 4, 4, 128, [1279, 1408], 128, "bf16"),    # one head a group
     (1, 3, 128, 2, 128, [3000], 32, "bf16"),           # 64 heads a group
 ]
 
