@@ -21,9 +21,9 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 constexpr int kEvictThreads = 1024, kEvictWarps = kEvictThreads / 32;
 
 // One CTA per (sequence, KV head): the `left`-th largest weight digit by digit
-// (11 + 11 + 10 bits), then the kept positions in ascending order. 64 heads of
-// 32768 weights take 27 us; four CTAs a head, joining their counters over
-// distributed shared memory, took 35 us (eight cluster barriers).
+// (11 + 11 + 10 bits), then the kept positions in ascending order. (Four CTAs a
+// head, joining their counters over distributed shared memory, were slower for
+// 64 heads of 32768 weights, 35 against 27 us: eight cluster barriers.)
 // CACHED: the keys stay in shared memory between the passes.
 constexpr int kEvictCached = 49152;  // keys
 template <bool CACHED>
@@ -53,13 +53,29 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
   const int m0 = p.sinks, m1 = n - p.recent;  // the others: m0 < m1, since sinks + recent <= budget < n
   int left = p.budget - p.sinks - p.recent;
   if constexpr (CACHED) {
-    for (int i0 = tid; i0 < n; i0 += 8 * kEvictThreads) {
-      float x[8];
+    if ((reinterpret_cast<uintptr_t>(w) & 15u) == 0) {
+      const int n4 = n >> 2;
+      for (int i0 = tid; i0 < n4; i0 += 8 * kEvictThreads) {  // 128 bytes per thread in flight
+        float4 x[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = i0 + k * kEvictThreads < n ? __ldg(w + i0 + k * kEvictThreads) : 0.f;
+        for (int k = 0; k < 8; ++k)
+          if (i0 + k * kEvictThreads < n4) x[k] = __ldg(reinterpret_cast<const float4*>(w) + i0 + k * kEvictThreads);
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (i0 + k * kEvictThreads < n) cached[i0 + k * kEvictThreads] = weight_key(x[k]);
+        for (int k = 0; k < 8; ++k)
+          if (i0 + k * kEvictThreads < n4)
+            *reinterpret_cast<uint4*>(&cached[4 * (i0 + k * kEvictThreads)]) =
+                make_uint4(weight_key(x[k].x), weight_key(x[k].y), weight_key(x[k].z), weight_key(x[k].w));
+      }
+      for (int i = 4 * n4 + tid; i < n; i += kEvictThreads) cached[i] = weight_key(__ldg(w + i));
+    } else {
+      for (int i0 = tid; i0 < n; i0 += 8 * kEvictThreads) {
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = i0 + k * kEvictThreads < n ? __ldg(w + i0 + k * kEvictThreads) : 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (i0 + k * kEvictThreads < n) cached[i0 + k * kEvictThreads] = weight_key(x[k]);
+      }
     }
     __syncthreads();
   }
@@ -72,6 +88,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
       for (int i = tid; i < 2048; i += kEvictThreads) hist[i] = 0u;
       __syncthreads();
+#pragma unroll 4
       for (int i = m0 + tid; i < m1; i += kEvictThreads) {
         const uint32_t k = key_of(i);
         if (pass == 0 || (k >> (shift + bits)) == (prefix >> (shift + bits))) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
@@ -114,22 +131,35 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
     }
   };
   int gt0 = 0, eq0 = 0;
+#pragma unroll 4
   for (int j = j0; j < j1; j += 32) {
     bool g, e;
     flags(j + lane, g, e);
-    gt0 += __popc(__ballot_sync(kFull, g));
-    eq0 += __popc(__ballot_sync(kFull, e));
+    const uint32_t bg = __ballot_sync(kFull, g), be = __ballot_sync(kFull, e);
+    // cached: the 32 keys have done their work, their first two places keep the verdicts
+    if (CACHED && lane < 2 && j + 1 < j1) cached[j + lane] = lane ? be : bg;
+    gt0 += __popc(bg);
+    eq0 += __popc(be);
   }
   if (lane == 0) warp_gt[warp] = gt0, warp_eq[warp] = eq0;
   __syncthreads();
   gt0 = eq0 = 0;
   for (int i = 0; i < warp; ++i) gt0 += warp_gt[i], eq0 += warp_eq[i];
   const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 4
   for (int j = j0; j < j1; j += 32) {
-    bool g, e;
-    flags(j + lane, g, e);
-    const uint32_t bg = __ballot_sync(kFull, g), be = __ballot_sync(kFull, e);
+    uint32_t bg, be;
+    if (CACHED && j + 1 < j1) {
+      bg = cached[j];
+      be = cached[j + 1];
+    } else {  // (a run's lone last key is still there)
+      bool g, e;
+      flags(j + lane, g, e);
+      bg = __ballot_sync(kFull, g);
+      be = __ballot_sync(kFull, e);
+    }
     const int eqr = eq0 + __popc(be & below);
+    const bool g = (bg >> lane) & 1u, e = (be >> lane) & 1u;
     if (g || (e && eqr < left)) keep[gt0 + __popc(bg & below) + min(eqr, left)] = j + lane;
     gt0 += __popc(bg);
     eq0 += __popc(be);
