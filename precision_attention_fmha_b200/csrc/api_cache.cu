@@ -372,7 +372,7 @@ fmha_status fmha_fwd_tree(const fmha_cache_args* a, const uint8_t* tree_mask, in
     AttnParams ap;
     CUtensorMap tq, tkp, tvp;
     if ((st = packed_params(a, p, t, &ap, &tq, &tkp, &tvp)) != FMHA_OK) return st;
-    e = launch_attention_packed(QK_BF16, PV_BF16, p.c.page_table != nullptr, ap, tq, tkp, tvp, tq, stream);
+    e = launch_attention_ragged(p.c.page_table != nullptr, ap, tq, tkp, tvp, stream);
     if (e == cudaSuccess) e = launch_cache_tail(p, tk, tv, stream);
   } else {
     p.part_lse = p.part_o + size_t(2) * t.n_ctas * t.rows * a->D;

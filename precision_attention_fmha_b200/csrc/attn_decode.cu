@@ -21,6 +21,13 @@ cudaError_t launch_attention_packed(int qk, int pv, bool paged, const AttnParams
   return cudaErrorInvalidValue;
 }
 
+cudaError_t launch_attention_ragged(bool paged, const AttnParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
+                                    const CUtensorMap& tv, cudaStream_t s) {
+  // No output map: every tile writes a partial (p.n_parts > 1).
+  return paged ? launch_attention_t<AttnCfg<128, QK_BF16, PV_BF16, true, false, true, false, 128, true>>(p, tq, tk, tv, tq, s)
+               : launch_attention_t<AttnCfg<128, QK_BF16, PV_BF16, false, false, true, false, 128, true>>(p, tq, tk, tv, tq, s);
+}
+
 namespace {
 
 // One warp per output row (b, token, head): lane l owns d = 4l .. 4l+3.

@@ -48,12 +48,15 @@ namespace fmha {
 
 // D: head dim of Q and K; DV: head dim of V and O (192 / 128 for a wide QK).
 template <int D_, int QK_, int PV_, bool PAGED_, bool P2_ = false, bool PACKED_ = false, bool O8_ = false,
-          int DV_ = D_>
+          int DV_ = D_, bool RAGGED_ = false>
 struct AttnCfg {
   static constexpr int D = D_, DV = DV_, QK = QK_, PV = PV_;
   static constexpr bool PAGED = PAGED_;
   // GQA-packed query tiles and split-KV ranges (decode shapes).
   static constexpr bool PACKED = PACKED_;
+  // Packed tiles over sequences of different lengths (p.ctx_lens, p.q_lens), partial results only.
+  static constexpr bool RAGGED = RAGGED_;
+  static_assert(!RAGGED || PACKED, "ragged contexts come in packed tiles");
   static constexpr bool P2 = P2_;  // E4M3 P split into two terms (hi + lo), each with its own PV product
   static_assert(!P2 || PV == PV_E4M3, "two-term P needs an E4M3 V");
   // E4M3 output: O / sf_o rounded to E4M3 (one 128-byte row per query row).
@@ -1485,7 +1488,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     item /= p.n_splits;
     hkv = item % p.Hkv;
     b = item / p.Hkv;
-    if (p.ctx_lens != nullptr && p.B <= 32) {
+    if (C::RAGGED && p.B <= 32) {
       // Sequences of different lengths: the longest start first, so that the
       // last CTAs to end are short ones (lane l ranks sequence l).
       const int len = lane < p.B ? __ldg(p.ctx_lens + lane) : -1;
@@ -1509,7 +1512,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int last = min(t[x].tok0 + toks - 1, p.Sq - 1) + (p.Skv - p.Sq);
         n = last < 0 ? 0 : min(p.n_kv_blocks, last / C::BN + 1);
       }
-      if (p.ctx_lens != nullptr) {
+      if constexpr (C::RAGGED) {
         n = min(max(__ldg(p.ctx_lens + b), 0) / C::BN, n);
         if (p.q_lens != nullptr && t[x].tok0 >= __ldg(p.q_lens + b)) t[x].valid = false;  // padding rows only
       }

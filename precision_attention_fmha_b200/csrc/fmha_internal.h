@@ -69,10 +69,10 @@ struct AttnParams {
   // tiles hold the same rows and take alternate kept KV tiles of the split;
   // each is then its own partial (n_parts = 2 * n_splits), else n_parts = n_splits.
   int32_t n_splits, split_tiles, kv_interleave, n_parts;
-  // Packed, nullable [B]: sequence b has only its first ctx_lens[b] / 128 whole
-  // key tiles here (the rest is another kernel's); Skv then bounds them all.
+  // Ragged packed tiles: [B], sequence b has its first ctx_lens[b] / 128 whole
+  // key tiles here (the rest is another kernel's), and Skv bounds them all.
   const int32_t* ctx_lens;
-  const int32_t* q_lens;  // with ctx_lens, nullable [B]: query tokens in use; a tile of later ones writes nothing
+  const int32_t* q_lens;  // nullable [B]: query tokens in use; a tile of later ones writes nothing
   float* o_part;   // [n_parts, B, Sq, Hq, D] when n_parts > 1
   float* lse_part; // [n_parts, B, Hq, Sq]
   uint32_t* err;        // device error word
@@ -108,6 +108,8 @@ cudaError_t launch_channel_mean(const QuantParams& p, cudaStream_t stream);
 cudaError_t launch_attention_packed(int qk_kind, int pv_kind, bool paged, const AttnParams& p,
                                     const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                     const CUtensorMap& to, cudaStream_t stream);
+cudaError_t launch_attention_ragged(bool paged, const AttnParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
+                                    const CUtensorMap& tv, cudaStream_t stream);
 struct MergeParams {
   const float* o_part; const float* lse_part;
   uint16_t* o; int64_t o_sb, o_ss, o_sh;  // bf16 bits
