@@ -9,7 +9,8 @@ library is missing -- there is no fallback implementation.
 
 _BINDING_NAMES = (
     "fmha_fwd", "fmha_fwd_block_sparse", "fmha_fwd_paged", "fmha_quantize_blockwise",
-    "quantize_workspace_bytes", "get_device_error", "FmhaError", "load_library",
+    "quantize_workspace_bytes", "get_device_error", "FmhaError", "load_library", "fmha_fwd_tree",
+    "fmha_fwd_selected", "key_bounds", "select_blocks", "key_weights", "evict_select", "cache_compact",
 )
 
 
