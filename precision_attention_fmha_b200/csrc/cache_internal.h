@@ -118,7 +118,6 @@ struct SelectParams {
   int32_t n_blocks, block_shift, top, sinks, recent;
   int32_t q_tile, n_tiles;  // query tokens that share a pick; tiles of T
   int32_t cluster;          // CTAs per item
-  int32_t pad_blocks;       // n_blocks rounded up (shared-memory layout)
   int32_t* list;            // [B, T, Hkv, top], or
   uint8_t* mask;            // [B, Hkv, n_tiles, n_blocks]
 };
