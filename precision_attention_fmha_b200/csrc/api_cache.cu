@@ -169,7 +169,8 @@ bool tree_plan(const fmha_cache_args* a, int capacity, TreePlan* t) {
     t->units = t->interleave ? 1 : ceil_div(tiles128, 2);
     const int64_t base = static_cast<int64_t>(a->B) * a->Hkv * t->units;
     const int kv = ceil_div(capacity, 128);
-    // A few CTAs per SM even out the sequences' lengths; a split keeps at least 8 tiles.
+    // About one CTA per SM (16 x 64 rows: 434 us; with two 469, with three 579: more partial results to join than the
+    // evener lengths save); a split keeps at least 8 tiles.
     const int64_t want = (kPackedCtasPerSm * sm_count() + base - 1) / base;
     t->n_splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(want, kv / 8)));
     t->n_parts = t->n_splits * (t->interleave ? 2 : 1);
@@ -225,7 +226,6 @@ fmha_status check_block(int block) {
   return FMHA_OK;
 }
 
-constexpr int kMaxPickBlocks = 16384;  // their 64-bit scores fit one CTA's shared memory
 // Query tokens from which fmha_key_weights runs on the tensor cores' 128-token tiles.
 constexpr int kManyQueries = 64;
 
@@ -249,7 +249,8 @@ size_t weight_bytes(const fmha_cache_args* a, const WeightRuns& r, int n_weights
 }
 
 // CTAs that score the blocks of one item: up to three per SM, while each keeps at least the 32 blocks that its warps
-// load at once (items 256, 512 blocks: one CTA each 34 us, two 22 us).
+// load at once. 256 items of 512 blocks, with the attention after them: one CTA 66.4 us, two 64.5, four 72.4; 512 items
+// of 64: one CTA 271, two 292.
 int pick_cluster(int64_t items, int n_blocks) {
   int c = 1;
   while (c < 8 && items * c < 3 * sm_count() && n_blocks / (2 * c) >= 32) c *= 2;

@@ -9,11 +9,14 @@
 // tile is read once for all query heads that share it.
 //
 // Work: items (sequence, [token,] KV head, row tile) x 64-key tiles. In tree
-// mode the tiles of all items form one list that the CTAs share evenly, so a
-// batch of very different lengths keeps every SM busy; the lengths are read on
-// the device, and a launch can be captured and replayed with others. A CTA
-// holds at most two partial items (its first and its last); their O / l and
-// log-sum-exp go to the workspace and a second kernel merges them.
+// mode the tiles of all sequences form one list that groups of CTAs (one CTA
+// per KV head and row tile) share evenly, so a batch of very different lengths
+// keeps every SM busy and the heads of a token are read side by side; the
+// lengths are read on the device, and a launch can be captured and replayed
+// with others. A CTA holds at most two partial items (its first and its last);
+// their O / l and log-sum-exp go to the workspace and a second kernel merges
+// them. In tail mode the whole tiles of the contexts are another kernel's: this
+// one takes the rest, and joins both parts itself.
 //
 // 160 threads: four MMA warps and one TMA producer warp feeding a ring of
 // 64-key slots.
@@ -68,6 +71,10 @@ __device__ __forceinline__ Row row_of(const CacheAttnParams& p, const Seg& g, in
   const int t = i / p.c.G;
   return t < p.c.T ? Row{t, g.hkv * p.c.G + i - t * p.c.G} : Row{-1, 0};
 }
+
+// A hidden score is -inf, which a factor of zero (a head whose scale is zero)
+// would turn into a NaN: the smallest normal number gives the other scores' zeros.
+__device__ __forceinline__ float score_factor(float c) { return c == 0.f ? 0x1p-126f : c; }
 
 // Two fp32 -> the 16-bit pair the PV product takes.
 template <class C>
@@ -154,7 +161,7 @@ __device__ void consume(const CacheAttnParams& p, uint8_t* ring, float* red, CaM
       rows[h] = row_of<C>(p, g, wm * 16 + gq + 8 * h);
       const uint16_t* src = p.q + g.b * p.q_sb + rows[h].tok * p.q_ss + rows[h].head * p.q_sh;
       load_q<C::K8, KS, 4>(qf, h, cs[h], src, rows[h].tok >= 0, j);
-      cs[h] *= p.scale_log2 * sfk;
+      cs[h] = score_factor(cs[h] * (p.scale_log2 * sfk));
     }
     const uint8_t* mask_row[2];
 #pragma unroll
@@ -590,7 +597,7 @@ __device__ void consume_t(const CacheAttnParams& p, uint8_t* ring, float* red, C
       load_q<C::K8, KS, 2>(qf[n], 0, f, p.q + g.b * p.q_sb + ro.tok * p.q_ss + ro.head * p.q_sh, ro.tok >= 0, j);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        cs[n][e] = p.scale_log2 * sfk * __shfl_sync(kFull, f, 4 * (2 * j + e));
+        cs[n][e] = score_factor(p.scale_log2 * sfk * __shfl_sync(kFull, f, 4 * (2 * j + e)));
         tok[n][e] = __shfl_sync(kFull, ro.tok, 4 * (2 * j + e));
       }
     }

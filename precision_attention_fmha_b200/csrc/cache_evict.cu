@@ -343,7 +343,8 @@ cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t s) {
   const int n = std::min(p.c.capacity, p.n_weights);
   if (n <= kEvictCached) {
     const int smem = std::max(n, 1) * 4;
-    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // The limit is the kernel's, not the launch's: calls of other sizes may be under way on other threads.
+    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvictCached * 4);
     if (e != cudaSuccess) return e;
     evict_select_kernel<true><<<p.c.B * p.c.Hkv, kEvictThreads, smem, s>>>(p);
   } else {

@@ -111,6 +111,7 @@ struct KeyBoundsParams {
 cudaError_t launch_key_bounds(int D, bool k8, const KeyBoundsParams& p, cudaStream_t stream);
 
 // Blocks picked for each query tile.
+constexpr int kMaxPickBlocks = 16384;  // their 64-bit scores fit one CTA's shared memory
 struct SelectParams {
   CacheView c;
   const uint16_t* q; int64_t q_sb, q_ss, q_sh;

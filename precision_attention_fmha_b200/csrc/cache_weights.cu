@@ -165,7 +165,8 @@ __global__ void __launch_bounds__(C::THREADS, 3)
 // per SM draw (key tile, run) items from a counter, the largest first, and a
 // run's sums go to the workspace, where they are added in order.
 // (A share of the exponentials as polynomials on the FMA pipe made it slower:
-// 280 us without, 285 with a quarter, 312 with half: issue slots bound it.)
+// 285 us with a quarter, 312 with half, when it took 280 without: issue
+// slots bound it.) Now 255 us.
 template <int D_>
 struct KmCfg {
   static constexpr int D = D_;

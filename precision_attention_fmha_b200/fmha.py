@@ -404,6 +404,23 @@ class _CacheArgs(ctypes.Structure):
 # The same layout as packed values: one call fills the 45 members, where setting them one by one in the structure
 # took 16 us of a decoding step's host time (packed: 5 us).
 _CACHE_ARGS = struct.Struct("@" + 4 * "Pii3q" + 2 * "Pii" + "6i3P3ifP")
+
+
+def _pack(*fields):
+    try:
+        return _CACHE_ARGS.pack(*fields)
+    except struct.error as e:
+        raise ValueError(f"a size of the cache or the queries is out of range: {e}") from None
+
+
+def _int32(x, what):
+    """x as an int that a 32-bit argument holds (ctypes would drop the higher bits)."""
+    x = int(x)
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError(f"{what} = {x} is out of range")
+    return x
+
+
 _NO_TENSOR, _NO_SF = (0, 0, 0, 0, 0, 0), (0, 0, 0)
 _DTYPES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float8_e4m3fn: E4M3, torch.int8: INT8}
 
@@ -516,7 +533,7 @@ def _cache_args(k, lens, page_table, q=None, v=None, out=None, q_lens=None, sf_k
         if out.shape != q.shape:
             raise ValueError(f"out {list(out.shape)} differs from q {list(q.shape)} in shape")
         to = _packed(out)
-    args = _CACHE_ARGS.pack(*tq, *tk, *tv, *to, *_cache_sf(sf_k, B, Hkv, "sf_k"), *_cache_sf(sf_v, B, Hkv, "sf_v"),
+    args = _pack(*tq, *tk, *tv, *to, *_cache_sf(sf_k, B, Hkv, "sf_k"), *_cache_sf(sf_v, B, Hkv, "sf_v"),
                             B, T, Hq, Hkv, D, capacity, _ints(lens, (B,), "lens"), _ints(q_lens, (B,), "q_lens"),
                             table[0], table[1], table[2], table[3], float(softmax_scale) if softmax_scale else 0.0,
                             lse_ptr)
@@ -558,7 +575,7 @@ def fmha_fwd_tree(q, k, v, ctx_lens, tree_mask=None, tree_lens=None, page_table=
         mask, mask_sb = tree_mask.data_ptr(), st[0] if tree_mask.shape[0] > 1 else 0
     lib = load_library()
     with _launch(stream, q, k, v, ctx_lens, tree_mask, tree_lens, page_table, out, lse, *_sf_tensors(sf_k, sf_v)) as s:
-        out = q.new_empty(q.shape, dtype=torch.bfloat16) if out is None else out
+        out = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else out
         a, _ = _cache_args(k, ctx_lens, page_table, q=q, v=v, out=out, q_lens=tree_lens, sf_k=sf_k, sf_v=sf_v,
                            softmax_scale=softmax_scale, lse=lse)
         workspace, ptr, size = _scratch(workspace, lib.fmha_fwd_tree_workspace_bytes(a), q)
@@ -581,15 +598,15 @@ def fmha_fwd_selected(q, k, v, blocks, lens, block, q_lens=None, page_table=None
     the q_lens[b] (None: T) query tokens are its last ones, and each sees keys up to its own position."""
     if blocks.dim() != 4:
         raise ValueError("blocks must be a contiguous int32 [B, T, Hkv, top] tensor")
-    top = blocks.shape[3]
+    top, block = _int32(blocks.shape[3], "top"), _int32(block, "block")
     ids = _ints(blocks, (q.shape[0], q.shape[1], k.shape[2], top), "blocks")
     lib = load_library()
     with _launch(stream, q, k, v, blocks, lens, q_lens, page_table, out, lse, *_sf_tensors(sf_k, sf_v)) as s:
-        out = q.new_empty(q.shape, dtype=torch.bfloat16) if out is None else out
+        out = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else out
         a, _ = _cache_args(k, lens, page_table, q=q, v=v, out=out, q_lens=q_lens, sf_k=sf_k, sf_v=sf_v,
                            softmax_scale=softmax_scale, lse=lse)
-        workspace, ptr, size = _scratch(workspace, lib.fmha_fwd_selected_workspace_bytes(a, top, int(block)), q)
-        _check(lib.fmha_fwd_selected(a, ids, top, int(block), ptr, size, s))
+        workspace, ptr, size = _scratch(workspace, lib.fmha_fwd_selected_workspace_bytes(a, top, block), q)
+        _check(lib.fmha_fwd_selected(a, ids, top, block, ptr, size, s))
     return out
 
 
@@ -600,6 +617,7 @@ def key_bounds(k, lens, block, page_table=None, bounds=None, start=None, stream=
     [B, Hkv, n_blocks, 2, D] (minima, maxima); blocks past a sequence's end are left as they were (zeros when
     allocated here). start: int32 [B]: blocks that end at or before it are left, so that a step refreshes the
     newest block only."""
+    block = _int32(block, "block")
     a, (B, Hkv, D, capacity) = _cache_args(k, lens, page_table)
     if bounds is None:
         shape = (B, Hkv, -(-capacity // block) if block > 0 else 0, 2, D)
@@ -613,7 +631,7 @@ def key_bounds(k, lens, block, page_table=None, bounds=None, start=None, stream=
     with _launch(stream, k, lens, page_table, bounds, start) as s:
         if bounds is None:
             bounds = torch.zeros(shape, dtype=torch.bfloat16, device=k.device)
-        _check(lib.fmha_key_bounds(a, bounds.data_ptr(), shape[2], int(block), start_ptr, s))
+        _check(lib.fmha_key_bounds(a, bounds.data_ptr(), _int32(shape[2], "n_blocks"), block, start_ptr, s))
     return bounds
 
 
@@ -630,17 +648,19 @@ def select_blocks(q, bounds, lens, block, top, sink_blocks=0, recent_blocks=1, q
             or q.dim() != 4 or bounds.shape[0] != q.shape[0] or bounds.shape[4] != q.shape[3]):
         raise ValueError("bounds must be contiguous BF16 [B, Hkv, n_blocks, 2, D] for q [B, T, Hq, D]")
     B, T, Hq, D = q.shape
-    Hkv, n_blocks = bounds.shape[1], bounds.shape[2]
-    a = _CACHE_ARGS.pack(*_packed(q), *(3 * _NO_TENSOR), *_NO_SF, *_NO_SF, B, T, Hq, Hkv, D, 0,
+    Hkv, n_blocks = bounds.shape[1], _int32(bounds.shape[2], "n_blocks")
+    block, top, q_tile = _int32(block, "block"), _int32(top, "top"), _int32(q_tile, "q_tile")
+    sink_blocks, recent_blocks = _int32(sink_blocks, "sink_blocks"), _int32(recent_blocks, "recent_blocks")
+    a = _pack(*_packed(q), *(3 * _NO_TENSOR), *_NO_SF, *_NO_SF, B, T, Hq, Hkv, D, 0,
                          _ints(lens, (B,), "lens"), _ints(q_lens, (B,), "q_lens"), 0, 0, 0, 0, 0.0, 0)
-    shape, dtype = ((B, T, Hkv, int(top)), torch.int32) if q_tile == 1 else ((B, Hkv, -(-T // 128), n_blocks), torch.uint8)
+    shape, dtype = ((B, T, Hkv, top), torch.int32) if q_tile == 1 else ((B, Hkv, -(-T // 128), n_blocks), torch.uint8)
     _array(out, dtype, shape, "out")
     lib = load_library()
     with _launch(stream, q, bounds, lens, q_lens, out) as s:
         if out is None:
             out = q.new_empty([max(0, n) for n in shape], dtype=dtype)
-        _check(lib.fmha_select_blocks(a, bounds.data_ptr(), n_blocks, int(block), int(top),
-                                      int(sink_blocks), int(recent_blocks), int(q_tile), out.data_ptr(), s))
+        _check(lib.fmha_select_blocks(a, bounds.data_ptr(), n_blocks, block, top, sink_blocks,
+                                      recent_blocks, q_tile, out.data_ptr(), s))
     return out
 
 
@@ -657,7 +677,7 @@ def key_weights(q, k, lse, weights, lens, q_lens=None, page_table=None, causal=T
     w = _floats(weights, (B, Hkv, weights.shape[2]), "weights")
     lib = load_library()
     with _launch(stream, q, k, lse, weights, lens, q_lens, page_table, *_sf_tensors(sf_k)) as s:
-        n, causal = weights.shape[2], 1 if causal else 0
+        n, causal = _int32(weights.shape[2], "n"), 1 if causal else 0
         workspace, ptr, size = _scratch(workspace, lib.fmha_key_weights_workspace_bytes(a, n, causal), q)
         _check(lib.fmha_key_weights(a, w, n, causal, 1 if accumulate else 0, ptr, size, s))
     return weights
@@ -672,7 +692,8 @@ def evict_select(weights, lens, budget, sinks=0, recent=0, keep=None, counts=Non
     if weights.dim() != 3:
         raise ValueError("weights must be a contiguous float32 [B, Hkv, n] tensor")
     B, Hkv, n = weights.shape
-    a = _CACHE_ARGS.pack(*(4 * _NO_TENSOR), *_NO_SF, *_NO_SF, B, 0, 0, Hkv, 0, 0, _ints(lens, (B,), "lens"),
+    n, budget, sinks, recent = _int32(n, "n"), _int32(budget, "budget"), _int32(sinks, "sinks"), _int32(recent, "recent")
+    a = _pack(*(4 * _NO_TENSOR), *_NO_SF, *_NO_SF, B, 0, 0, Hkv, 0, 0, _ints(lens, (B,), "lens"),
                          0, 0, 0, 0, 0, 0.0, 0)
     w = _floats(weights, (B, Hkv, n), "weights")
     _ints(keep, (B, Hkv, budget), "keep")
@@ -682,9 +703,8 @@ def evict_select(weights, lens, budget, sinks=0, recent=0, keep=None, counts=Non
         if keep is None:
             keep = weights.new_empty((B, Hkv, max(0, budget)), dtype=torch.int32)
         if counts is None:
-            counts = weights.new_empty((B,), dtype=torch.int32)
-        _check(lib.fmha_evict_select(a, w, n, int(budget), int(sinks), int(recent), keep.data_ptr(),
-                                     counts.data_ptr(), s))
+            counts = torch.empty_like(lens)
+        _check(lib.fmha_evict_select(a, w, n, budget, sinks, recent, keep.data_ptr(), counts.data_ptr(), s))
     return keep, counts
 
 
@@ -727,5 +747,6 @@ def cache_compact(k, v, keep, counts, dst_start=None, page_table=None, k_out=Non
                  weights_out) as s:
         _check(lib.fmha_cache_compact(a, o, keep.data_ptr(),
                                       keep.stride(0) if B > 1 else 0, keep.stride(1) if keep.shape[1] > 1 else 0,
-                                      keep.shape[2], counts.data_ptr(), start, w, nw, wo, nwo, s))
+                                      _int32(keep.shape[2], "n_keep"), counts.data_ptr(), start, w,
+                                      _int32(nw, "n"), wo, _int32(nwo, "n"), s))
     return (k, v) if k_out is None else (k_out, v_out)

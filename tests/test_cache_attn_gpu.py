@@ -211,3 +211,20 @@ def test_tree_e4m3_visible_nan_codes_reach_their_rows():
     o[0, 0, :2], o[0, 1, 2:, 5] = 0, 0
     lse[0, :2, 0] = 0
     assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("T", [1, 9])  # 2 and 18 rows: both arrangements of the few-row kernel
+def test_zero_scale(T):
+    """A KV head whose key scale is zero: every key in sight weighs the same, also beside keys that are not."""
+    from precision_attention_fmha_b200 import fmha
+
+    q, k, v, (_, sv), g = make(21, 2, T, 4, 2, 64, 200, 0, "e4m3")
+    sk = fmha.Scale(torch.tensor([[0.0, 0.03], [0.02, 0.0]], device=DEV), "per_head")
+    ctx = [70, 130]
+    lse = torch.empty(2, 4, T, device=DEV)
+    o = fmha.fmha_fwd_tree(q, k, v, i32(ctx), sf_k=sk, sf_v=sv, lse=lse)
+    ref.check(o, lse, ref.tree(q, k, v, ctx, None, None, None, sk, sv), v8=True)
+    lens = [c + T for c in ctx]
+    ids = torch.tensor([0, 3, 2, 7], dtype=torch.int32, device=DEV).expand(2, T, 2, 4).contiguous()
+    o = fmha.fmha_fwd_selected(q, k, v, ids, i32(lens), 16, sf_k=sk, sf_v=sv, lse=lse)
+    ref.check(o, lse, ref.selected(q, k, v, ids, lens, 16, None, None, sk, sv), v8=True)

@@ -212,3 +212,23 @@ def test_binding_checks_shapes():
     refused(fmha.cache_compact, k, k, torch.zeros(2, 4, 2, dtype=i32), lens, k_out=k)
     refused(fmha.cache_compact, k, k, torch.zeros(2, 4, 2, dtype=i32), lens, weights_out=torch.zeros(2, 4, 9))
     refused(fmha.fmha_fwd_tree, q, k, k, lens, sf_k=fmha.Scale(torch.zeros(3, 3), "per_head"))
+
+
+def test_numbers_that_32_bits_do_not_hold():
+    """Sizes past a 32-bit argument are refused, not cut to their low bits."""
+    big = (1 << 32) + 4
+    lens = torch.zeros(1, dtype=torch.int32)
+    w = torch.zeros(1, 1, 8)
+    q = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16)
+    k = torch.zeros(1, 128, 1, 64, dtype=torch.bfloat16)
+    bounds = torch.zeros(1, 1, 8, 2, 64, dtype=torch.bfloat16)
+    for f in (lambda: fmha.evict_select(w, lens, big), lambda: fmha.evict_select(w, lens, 4, sinks=big),
+              lambda: fmha.evict_select(w, lens, 4, recent=big), lambda: fmha.key_bounds(k, lens, big),
+              lambda: fmha.select_blocks(q, bounds, lens, big, 4), lambda: fmha.select_blocks(q, bounds, lens, 16, big),
+              lambda: fmha.select_blocks(q, bounds, lens, 16, 4, sink_blocks=big),
+              lambda: fmha.select_blocks(q, bounds, lens, 16, 4, recent_blocks=big),
+              lambda: fmha.select_blocks(q, bounds, lens, 16, 4, q_tile=big),
+              lambda: fmha.fmha_fwd_selected(q, k, k, torch.zeros(1, 1, 1, 2, dtype=torch.int32), lens, big),
+              lambda: fmha.key_bounds(k, lens, 16, page_table=torch.empty(1, 1 << 25, dtype=torch.int32))):
+        with pytest.raises(ValueError, match="out of range"):
+            f()

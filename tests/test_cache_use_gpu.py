@@ -81,6 +81,48 @@ def test_streams_and_threads():
         assert all(torch.equal(a, b) for a, b in zip(r, want))
 
 
+def test_threads_with_calls_of_different_sizes():
+    """The kernels whose shared memory follows the call's size: large and small calls under way at once."""
+    import threading
+
+    from precision_attention_fmha_b200 import fmha
+
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    sizes = [40, 45000, 3000, 20000]
+    cases = []
+    for n in sizes:
+        w = torch.rand(1, 2, n, generator=g, device=DEV)
+        n_blocks = max(4, n // 4)
+        q = torch.randn(1, 1, 4, 64, generator=g, device=DEV).bfloat16()
+        bounds = torch.randn(1, 2, n_blocks, 2, 64, generator=g, device=DEV).bfloat16()
+        cases.append((w, i32([n]), q, bounds, i32([n_blocks * 16])))
+
+    def work(c, stream=None):
+        w, lens, q, bounds, tokens = c
+        return fmha.evict_select(w, lens, 17, stream=stream)[0], fmha.select_blocks(q, bounds, tokens, 16, 3, stream=stream)
+
+    want = [work(c) for c in cases]
+    torch.cuda.synchronize()
+    errors, got = [], [None] * len(cases)
+
+    def run(i):
+        try:
+            stream = torch.cuda.Stream()
+            for _ in range(200):
+                got[i] = work(cases[i], stream)
+            stream.synchronize()
+        except Exception as e:  # an assertion of the main thread reports it
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(cases))]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not errors
+    for r, x in zip(got, want):
+        assert all(torch.equal(a, b) for a, b in zip(r, x))
+
+
 def test_graph_replay_with_grown_sequences():
     """One capture; between replays the lengths, keys and queries change in place."""
     from precision_attention_fmha_b200 import fmha
@@ -166,6 +208,21 @@ def test_far_positions():
     before = k[1, n - 40:n].clone()
     fmha.cache_compact(k, v, keep, i32([40, 40]), dst_start=i32([5, n - 100]))
     assert torch.equal(k[1, n - 100:n - 60], before)
+    fmha.get_device_error()
+
+
+def test_bounds_with_far_more_blocks_than_keys():
+    """Room for more blocks than 32-bit positions reach: what lies past the cache is left as it was."""
+    from precision_attention_fmha_b200 import fmha
+
+    n = (1 << 24) + 3
+    k = torch.randn(1, 300, 1, 64, device=DEV).bfloat16()
+    bounds = torch.empty(1, 1, n, 2, 64, dtype=torch.bfloat16, device=DEV)
+    bounds[0, 0, 3:] = 7
+    fmha.key_bounds(k, i32([300]), 128, bounds=bounds)
+    first = fmha.key_bounds(k, i32([300]), 128)
+    assert torch.equal(bounds[:, :, :3], first)
+    assert bool((bounds[0, 0, 3:] == 7).all())
     fmha.get_device_error()
 
 
