@@ -23,7 +23,9 @@ constexpr int kEvictThreads = 1024, kEvictWarps = kEvictThreads / 32;
 // One CTA per (sequence, KV head): the `left`-th largest weight digit by digit
 // (11 + 11 + 10 bits), then the kept positions in ascending order. (Four CTAs a
 // head, joining their counters over distributed shared memory, were slower for
-// 64 heads of 32768 weights, 35 against 27 us: eight cluster barriers.)
+// 64 heads of 32768 weights, 35 against 27 us: eight cluster barriers.) 20 us
+// for those: a seventh of it the weights' way here, the rest the passes of one
+// SM a head.
 // CACHED: the keys stay in shared memory between the passes.
 constexpr int kEvictCached = 49152;  // keys
 template <bool CACHED>
@@ -80,7 +82,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
     __syncthreads();
   }
   auto key_of = [&](int i) { return CACHED ? cached[i] : weight_key(__ldg(w + i)); };
-  uint32_t limit = 0xffffffffu;  // keys above it stay, and `left` of those equal to it
+  uint32_t limit = 0xfffffffeu;  // keys above it stay, and `left` of those equal to it (no weight's key is as large)
   if (left > 0) {
     uint32_t prefix = 0;
 #pragma unroll 1
@@ -117,53 +119,69 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
     }
     limit = prefix;
   }
-  // Warps take consecutive runs of positions.
-  const int run = ((n + kEvictWarps - 1) / kEvictWarps + 31) & ~31;
+  // Warps take consecutive runs of positions, lanes words of them. A lane reads its word from its own number on, round, so
+  // that the lanes are in different banks (votes over neighbouring keys: 6900 clocks, not 5000). Long runs have words of
+  // 32 (words of run / 32 collide in the banks: 120 us for 8 x 8 heads of 25-33k keys with their move, not 111), short
+  // ones small words (2049 keys on 8 heads: 13.8 us with words of 32, else 11.8).
+  const int run = ((n + kEvictWarps - 1) / kEvictWarps + 31) & ~31, width = run > 256 ? 32 : run / 32;
+  const int step = 32 * width;
   const int j0 = min(n, warp * run), j1 = min(n, j0 + run);
-  auto flags = [&](int j, bool& gt, bool& eq) {
-    gt = eq = false;
-    if (j >= j1) return;
-    if (j < m0 || j >= m1) gt = true;
-    else {
-      const uint32_t k = key_of(j);
-      gt = k > limit;
-      eq = k == limit && left > 0;
+  auto verdicts = [&](int at, uint32_t& gt, uint32_t& eq) {
+    gt = eq = 0u;
+    if (at >= j1) return;
+    int x = lane % width;
+#pragma unroll 4  // a short loop: code that runs once waits for its instructions
+    for (int i = 0; i < width; ++i) {
+      const uint32_t k = key_of(min(at + x, n - 1));
+      gt |= (k > limit ? 1u : 0u) << x;
+      eq |= (k == limit ? 1u : 0u) << x;
+      x = x + 1 == width ? 0 : x + 1;
     }
+    auto below = [&](int j) { return j <= at ? 0u : j >= at + 32 ? kFull : (1u << (j - at)) - 1u; };
+    const uint32_t forced = below(m0) | ~below(m1), live = below(min(j1, at + width));
+    gt = (gt | forced) & live;
+    eq = eq & ~forced & live;
   };
+  uint32_t gt = 0u, eq = 0u;
   int gt0 = 0, eq0 = 0;
-#pragma unroll 4
-  for (int j = j0; j < j1; j += 32) {
-    bool g, e;
-    flags(j + lane, g, e);
-    const uint32_t bg = __ballot_sync(kFull, g), be = __ballot_sync(kFull, e);
-    // cached: the 32 keys have done their work, their first two places keep the verdicts
-    if (CACHED && lane < 2 && j + 1 < j1) cached[j + lane] = lane ? be : bg;
-    gt0 += __popc(bg);
-    eq0 += __popc(be);
+  for (int j = j0; j < j1; j += step) {
+    verdicts(j + width * lane, gt, eq);
+    gt0 += __reduce_add_sync(kFull, __popc(gt));
+    eq0 += __reduce_add_sync(kFull, __popc(eq));
   }
   if (lane == 0) warp_gt[warp] = gt0, warp_eq[warp] = eq0;
   __syncthreads();
-  gt0 = eq0 = 0;
-  for (int i = 0; i < warp; ++i) gt0 += warp_gt[i], eq0 += warp_eq[i];
-  const uint32_t below = (1u << lane) - 1u;
-#pragma unroll 4
-  for (int j = j0; j < j1; j += 32) {
-    uint32_t bg, be;
-    if (CACHED && j + 1 < j1) {
-      bg = cached[j];
-      be = cached[j + 1];
-    } else {  // (a run's lone last key is still there)
-      bool g, e;
-      flags(j + lane, g, e);
-      bg = __ballot_sync(kFull, g);
-      be = __ballot_sync(kFull, e);
+  gt0 = __reduce_add_sync(kFull, lane < warp ? warp_gt[lane] : 0);
+  eq0 = __reduce_add_sync(kFull, lane < warp ? warp_eq[lane] : 0);
+  // Listed in the keys' place, which have done their work, and written side by side from there.
+  const bool staged = CACHED && run <= step;
+  int32_t* list = staged ? reinterpret_cast<int32_t*>(cached) : keep;
+  for (int j = j0; j < j1; j += step) {
+    if (run > step) verdicts(j + width * lane, gt, eq);  // else the words are still here
+    // Verdicts of the words before: two counts of at most 1024 in one word.
+    const uint32_t mine = __popc(gt) | __popc(eq) << 16;
+    uint32_t before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(kFull, before, o);
+      if (lane >= o) before += v;
     }
-    const int eqr = eq0 + __popc(be & below);
-    const bool g = (bg >> lane) & 1u, e = (be >> lane) & 1u;
-    if (g || (e && eqr < left)) keep[gt0 + __popc(bg & below) + min(eqr, left)] = j + lane;
-    gt0 += __popc(bg);
-    eq0 += __popc(be);
+    const uint32_t total = __shfl_sync(kFull, before, 31);
+    before -= mine;
+    const int eqr = eq0 + static_cast<int>(before >> 16), room_eq = max(0, left - eqr);
+    if (__popc(eq) > room_eq) {  // the first of them
+      uint32_t rest = eq;
+      for (int i = 0; i < room_eq; ++i) rest &= rest - 1u;
+      eq ^= rest;
+    }
+    int32_t* to = list + gt0 + static_cast<int>(before & 0xffffu) + min(eqr, left);
+    for (uint32_t word = gt | eq; word != 0u; word &= word - 1u) *to++ = j + width * lane + __ffs(word) - 1;
+    gt0 += static_cast<int>(total & 0xffffu);
+    eq0 += static_cast<int>(total >> 16);
   }
+  if (!staged) return;
+  __syncthreads();
+  for (int i = tid; i < count; i += kEvictThreads) keep[i] = list[i];
 }
 
 // ------------------------------------------------------------------ compact --
