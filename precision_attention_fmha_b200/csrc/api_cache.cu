@@ -440,7 +440,7 @@ fmha_status fmha_key_bounds(const fmha_cache_args* a, void* bounds, int32_t n_bl
   memset(&p, 0, sizeof(p));
   bool k8, v8;
   if ((st = check_cache(a, false, false, &p.c, &k8, &v8)) != FMHA_OK) return st;
-  if (static_cast<int64_t>(a->B) * a->Hkv * n_blocks >= (int64_t(1) << 33))
+  if (static_cast<int64_t>(a->B) * a->Hkv * n_blocks >= (int64_t(1) << 32))
     return fail(FMHA_ERR_UNSUPPORTED, "grid too large");
   if ((st = bind_device(&p.c)) != FMHA_OK) return st;
   p.k = static_cast<const uint8_t*>(a->k.ptr);
