@@ -508,35 +508,39 @@ def _cache_args(k, lens, page_table, q=None, v=None, out=None, q_lens=None, sf_k
     """fmha_cache_args of k (and v) [B, S, Hkv, D], or pools [pages, page_size, Hkv, D] with a page table
     [B, max_pages]; and (B, Hkv, D, capacity)."""
     tk = _packed(k)
-    n, rows, Hkv, D = k.shape
+    shape = k.shape
+    n, rows, Hkv, D = shape
     if page_table is not None:
-        if page_table.dim() != 2:
+        pages = page_table.shape
+        if len(pages) != 2:
             raise ValueError("page_table must be contiguous int32 [B, max_pages_per_seq]")
-        B, per = page_table.shape
-        table = (_ints(page_table, page_table.shape, "page_table"), n, rows, per)
+        B, per = pages
+        table = (_array(page_table, torch.int32, pages, "page_table"), n, rows, per)
         capacity = per * rows
     else:
         B, capacity, table = n, rows, (0, 0, 0, 0)
     tv = tq = to = _NO_TENSOR
     if v is not None:
-        if v.shape != k.shape:
-            raise ValueError(f"k {list(k.shape)} and v {list(v.shape)} differ in shape")
+        if v.shape != shape:
+            raise ValueError(f"k {list(shape)} and v {list(v.shape)} differ in shape")
         tv = _packed(v)
     T = Hq = lse_ptr = 0
     if q is not None:
         tq = _packed(q)
-        if q.shape[0] != B or q.shape[3] != D:
-            raise ValueError(f"q {list(q.shape)} does not fit a cache of {B} sequences with head dim {D}")
-        T, Hq = q.shape[1], q.shape[2]
-        lse_ptr = _floats(lse, (B, Hq, T), "lse")
-    if out is not None:
-        if out.shape != q.shape:
-            raise ValueError(f"out {list(out.shape)} differs from q {list(q.shape)} in shape")
-        to = _packed(out)
+        q_shape = q.shape
+        q_B, T, Hq, q_D = q_shape
+        if q_B != B or q_D != D:
+            raise ValueError(f"q {list(q_shape)} does not fit a cache of {B} sequences with head dim {D}")
+        if lse is not None:
+            lse_ptr = _array(lse, torch.float32, (B, Hq, T), "lse")
+        if out is not None:
+            if out.shape != q_shape:
+                raise ValueError(f"out {list(out.shape)} differs from q {list(q_shape)} in shape")
+            to = _packed(out)
     args = _pack(*tq, *tk, *tv, *to, *_cache_sf(sf_k, B, Hkv, "sf_k"), *_cache_sf(sf_v, B, Hkv, "sf_v"),
-                            B, T, Hq, Hkv, D, capacity, _ints(lens, (B,), "lens"), _ints(q_lens, (B,), "q_lens"),
-                            table[0], table[1], table[2], table[3], float(softmax_scale) if softmax_scale else 0.0,
-                            lse_ptr)
+                 B, T, Hq, Hkv, D, capacity, _array(lens, torch.int32, (B,), "lens"),
+                 _array(q_lens, torch.int32, (B,), "q_lens"), *table,
+                 float(softmax_scale) if softmax_scale else 0.0, lse_ptr)
     return args, (B, Hkv, D, capacity)
 
 
