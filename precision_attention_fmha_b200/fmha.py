@@ -403,6 +403,7 @@ class _CacheArgs(ctypes.Structure):
 
 # The same layout as packed values: one call fills the 45 members, where setting them one by one in the structure
 # took 16 us of a decoding step's host time (packed: 5 us).
+_NO_TABLE = (0, 0, 0, 0)
 _CACHE_ARGS = struct.Struct("@" + 4 * "Pii3q" + 2 * "Pii" + "6i3P3ifP")
 
 
@@ -413,12 +414,11 @@ def _pack(*fields):
         raise ValueError(f"a size of the cache or the queries is out of range: {e}") from None
 
 
-def _int32(x, what):
-    """x as an int that a 32-bit argument holds (ctypes would drop the higher bits)."""
-    x = int(x)
-    if not -(1 << 31) <= x < 1 << 31:
-        raise ValueError(f"{what} = {x} is out of range")
-    return x
+def _int32s(what, *values):
+    """Checks that 32-bit arguments hold the values (ctypes would drop their higher bits)."""
+    for x in values:
+        if not -0x80000000 <= x < 0x80000000:
+            raise ValueError(f"{what} {values}: a number is out of range")
 
 
 _NO_TENSOR, _NO_SF = (0, 0, 0, 0, 0, 0), (0, 0, 0)
@@ -503,27 +503,31 @@ def _cache_sf(s, B, Hkv, what):
     return (sf.ptr or 0, sf.kind, sf.rows_per_block)
 
 
-def _cache_args(k, lens, page_table, q=None, v=None, out=None, q_lens=None, sf_k=None, sf_v=None,
-                softmax_scale=None, lse=None):
-    """fmha_cache_args of k (and v) [B, S, Hkv, D], or pools [pages, page_size, Hkv, D] with a page table
-    [B, max_pages]; and (B, Hkv, D, capacity)."""
+def _cache_view(k, v, page_table):
+    """The tensor fields of k and v, and B, Hkv, D, capacity and the page table's fields."""
     tk = _packed(k)
     shape = k.shape
     n, rows, Hkv, D = shape
-    if page_table is not None:
-        pages = page_table.shape
-        if len(pages) != 2:
-            raise ValueError("page_table must be contiguous int32 [B, max_pages_per_seq]")
-        B, per = pages
-        table = (_array(page_table, torch.int32, pages, "page_table"), n, rows, per)
-        capacity = per * rows
-    else:
-        B, capacity, table = n, rows, (0, 0, 0, 0)
-    tv = tq = to = _NO_TENSOR
+    tv = _NO_TENSOR
     if v is not None:
         if v.shape != shape:
             raise ValueError(f"k {list(shape)} and v {list(v.shape)} differ in shape")
         tv = _packed(v)
+    if page_table is None:
+        return tk, tv, n, Hkv, D, rows, _NO_TABLE
+    pages = page_table.shape
+    if len(pages) != 2:
+        raise ValueError("page_table must be contiguous int32 [B, max_pages_per_seq]")
+    B, per = pages
+    return tk, tv, B, Hkv, D, per * rows, (_array(page_table, torch.int32, pages, "page_table"), n, rows, per)
+
+
+def _cache_args(k, lens, page_table, q=None, v=None, out=None, q_lens=None, sf_k=None, sf_v=None,
+                softmax_scale=None, lse=None):
+    """fmha_cache_args of k (and v) [B, S, Hkv, D], or pools [pages, page_size, Hkv, D] with a page table
+    [B, max_pages]; and (B, Hkv, D, capacity)."""
+    tk, tv, B, Hkv, D, capacity, table = _cache_view(k, v, page_table)
+    tq = to = _NO_TENSOR
     T = Hq = lse_ptr = 0
     if q is not None:
         tq = _packed(q)
@@ -602,7 +606,8 @@ def fmha_fwd_selected(q, k, v, blocks, lens, block, q_lens=None, page_table=None
     the q_lens[b] (None: T) query tokens are its last ones, and each sees keys up to its own position."""
     if blocks.dim() != 4:
         raise ValueError("blocks must be a contiguous int32 [B, T, Hkv, top] tensor")
-    top, block = _int32(blocks.shape[3], "top"), _int32(block, "block")
+    top, block = blocks.shape[3], int(block)
+    _int32s("top, block", top, block)
     ids = _ints(blocks, (q.shape[0], q.shape[1], k.shape[2], top), "blocks")
     lib = load_library()
     with _launch(stream, q, k, v, blocks, lens, q_lens, page_table, out, lse, *_sf_tensors(sf_k, sf_v)) as s:
@@ -621,7 +626,7 @@ def key_bounds(k, lens, block, page_table=None, bounds=None, start=None, stream=
     [B, Hkv, n_blocks, 2, D] (minima, maxima); blocks past a sequence's end are left as they were (zeros when
     allocated here). start: int32 [B]: blocks that end at or before it are left, so that a step refreshes the
     newest block only."""
-    block = _int32(block, "block")
+    block = int(block)
     a, (B, Hkv, D, capacity) = _cache_args(k, lens, page_table)
     if bounds is None:
         shape = (B, Hkv, -(-capacity // block) if block > 0 else 0, 2, D)
@@ -631,11 +636,12 @@ def key_bounds(k, lens, block, page_table=None, bounds=None, start=None, stream=
                 or not bounds.is_contiguous()):
             raise ValueError(f"bounds must be contiguous BF16 [{B}, {Hkv}, n_blocks, 2, {D}]")
     start_ptr = _ints(start, (B,), "start")
+    _int32s("n_blocks, block", shape[2], block)
     lib = load_library()
     with _launch(stream, k, lens, page_table, bounds, start) as s:
         if bounds is None:
             bounds = torch.zeros(shape, dtype=torch.bfloat16, device=k.device)
-        _check(lib.fmha_key_bounds(a, bounds.data_ptr(), _int32(shape[2], "n_blocks"), block, start_ptr, s))
+        _check(lib.fmha_key_bounds(a, bounds.data_ptr(), shape[2], block, start_ptr, s))
     return bounds
 
 
@@ -648,21 +654,22 @@ def select_blocks(q, bounds, lens, block, top, sink_blocks=0, recent_blocks=1, q
     q_tile 1: int32 [B, T, Hkv, top], ascending ids then -1, for ``fmha_fwd_selected``. q_tile 128 (block 128):
     the uint8 mask [B, Hkv, ceil(T/128), n_blocks] of ``fmha_fwd_block_sparse`` / ``fmha_fwd_paged``, picked by
     tiles of 128 query tokens."""
-    if (bounds.dtype != torch.bfloat16 or bounds.dim() != 5 or bounds.shape[3] != 2 or not bounds.is_contiguous()
-            or q.dim() != 4 or bounds.shape[0] != q.shape[0] or bounds.shape[4] != q.shape[3]):
+    shape, q_shape = bounds.shape, q.shape
+    if (bounds.dtype != torch.bfloat16 or len(shape) != 5 or shape[3] != 2 or not bounds.is_contiguous()
+            or len(q_shape) != 4 or shape[0] != q_shape[0] or shape[4] != q_shape[3]):
         raise ValueError("bounds must be contiguous BF16 [B, Hkv, n_blocks, 2, D] for q [B, T, Hq, D]")
-    B, T, Hq, D = q.shape
-    Hkv, n_blocks = bounds.shape[1], _int32(bounds.shape[2], "n_blocks")
-    block, top, q_tile = _int32(block, "block"), _int32(top, "top"), _int32(q_tile, "q_tile")
-    sink_blocks, recent_blocks = _int32(sink_blocks, "sink_blocks"), _int32(recent_blocks, "recent_blocks")
-    a = _pack(*_packed(q), *(3 * _NO_TENSOR), *_NO_SF, *_NO_SF, B, T, Hq, Hkv, D, 0,
-                         _ints(lens, (B,), "lens"), _ints(q_lens, (B,), "q_lens"), 0, 0, 0, 0, 0.0, 0)
+    B, T, Hq, D = q_shape
+    Hkv, n_blocks = shape[1], shape[2]
+    block, top, q_tile, sink_blocks, recent_blocks = int(block), int(top), int(q_tile), int(sink_blocks), int(recent_blocks)
+    _int32s("n_blocks, block, top, q_tile, sink_blocks, recent_blocks", n_blocks, block, top, q_tile, sink_blocks, recent_blocks)
+    a = _pack(*_packed(q), *_NO_TENSOR, *_NO_TENSOR, *_NO_TENSOR, *_NO_SF, *_NO_SF, B, T, Hq, Hkv, D, 0,
+              _ints(lens, (B,), "lens"), _ints(q_lens, (B,), "q_lens"), *_NO_TABLE, 0.0, 0)
     shape, dtype = ((B, T, Hkv, top), torch.int32) if q_tile == 1 else ((B, Hkv, -(-T // 128), n_blocks), torch.uint8)
     _array(out, dtype, shape, "out")
     lib = load_library()
     with _launch(stream, q, bounds, lens, q_lens, out) as s:
         if out is None:
-            out = q.new_empty([max(0, n) for n in shape], dtype=dtype)
+            out = q.new_empty(shape if top >= 0 else 0, dtype=dtype)
         _check(lib.fmha_select_blocks(a, bounds.data_ptr(), n_blocks, block, top, sink_blocks,
                                       recent_blocks, q_tile, out.data_ptr(), s))
     return out
@@ -679,9 +686,10 @@ def key_weights(q, k, lse, weights, lens, q_lens=None, page_table=None, causal=T
     if weights.dim() != 3:
         raise ValueError("weights must be a contiguous float32 [B, Hkv, n] tensor")
     w = _floats(weights, (B, Hkv, weights.shape[2]), "weights")
+    _int32s("n", weights.shape[2])
     lib = load_library()
     with _launch(stream, q, k, lse, weights, lens, q_lens, page_table, *_sf_tensors(sf_k)) as s:
-        n, causal = _int32(weights.shape[2], "n"), 1 if causal else 0
+        n, causal = weights.shape[2], 1 if causal else 0
         workspace, ptr, size = _scratch(workspace, lib.fmha_key_weights_workspace_bytes(a, n, causal), q)
         _check(lib.fmha_key_weights(a, w, n, causal, 1 if accumulate else 0, ptr, size, s))
     return weights
@@ -696,9 +704,10 @@ def evict_select(weights, lens, budget, sinks=0, recent=0, keep=None, counts=Non
     if weights.dim() != 3:
         raise ValueError("weights must be a contiguous float32 [B, Hkv, n] tensor")
     B, Hkv, n = weights.shape
-    n, budget, sinks, recent = _int32(n, "n"), _int32(budget, "budget"), _int32(sinks, "sinks"), _int32(recent, "recent")
-    a = _pack(*(4 * _NO_TENSOR), *_NO_SF, *_NO_SF, B, 0, 0, Hkv, 0, 0, _ints(lens, (B,), "lens"),
-                         0, 0, 0, 0, 0, 0.0, 0)
+    budget, sinks, recent = int(budget), int(sinks), int(recent)
+    _int32s("n, budget, sinks, recent", n, budget, sinks, recent)
+    a = _pack(*_NO_TENSOR, *_NO_TENSOR, *_NO_TENSOR, *_NO_TENSOR, *_NO_SF, *_NO_SF, B, 0, 0, Hkv, 0, 0,
+              _ints(lens, (B,), "lens"), 0, *_NO_TABLE, 0.0, 0)
     w = _floats(weights, (B, Hkv, n), "weights")
     _ints(keep, (B, Hkv, budget), "keep")
     _ints(counts, (B,), "counts")
@@ -723,34 +732,42 @@ def cache_compact(k, v, keep, counts, dst_start=None, page_table=None, k_out=Non
     Returns (k_out, v_out)."""
     if counts is None:
         raise ValueError("counts must be a contiguous int32 tensor")
-    a, (B, Hkv, _, _) = _cache_args(k, counts, page_table, v=v)
-    if keep.dtype != torch.int32 or keep.dim() != 3 or keep.shape[0] != B or keep.shape[1] not in (1, Hkv) or (
-            keep.shape[2] > 1 and keep.stride(2) != 1):
+    tk, tv, B, Hkv, D, capacity, table = _cache_view(k, v, page_table)
+    lens = _array(counts, torch.int32, (B,), "counts")
+    a = _pack(*_NO_TENSOR, *tk, *tv, *_NO_TENSOR, *_NO_SF, *_NO_SF, B, 0, 0, Hkv, D, capacity, lens, 0, *table, 0.0, 0)
+    shape, stride = keep.shape, keep.stride()
+    if keep.dtype != torch.int32 or len(shape) != 3 or shape[0] != B or shape[1] not in (1, Hkv) or (
+            shape[2] > 1 and stride[2] != 1):
         raise ValueError(f"keep must be int32 [{B}, {Hkv} or 1, n] with unit last stride")
-    start = _ints(dst_start, (B,), "dst_start")
+    start = _array(dst_start, torch.int32, (B,), "dst_start")
     if (k_out is None) != (v_out is None) or (k_out is None and (out_page_table is not None or weights_out is not None)):
         raise ValueError("another cache needs k_out and v_out (and, when paged, out_page_table)")
     o = 0
     if k_out is not None:
-        if k_out.dtype != k.dtype or v_out.dtype != v.dtype or k_out.shape[2:] != k.shape[2:]:
+        if k_out.dtype != k.dtype or v_out.dtype != v.dtype:
             raise ValueError("k_out / v_out must have the dtypes, heads and head dim of k / v")
-        o, _ = _cache_args(k_out, counts, out_page_table, v=v_out)
+        ok, ov, out_B, out_Hkv, out_D, room, out_table = _cache_view(k_out, v_out, out_page_table)
+        if out_Hkv != Hkv or out_D != D:
+            raise ValueError("k_out / v_out must have the dtypes, heads and head dim of k / v")
+        if out_B != B:
+            raise ValueError(f"caches of {B} and {out_B} sequences")
+        o = _pack(*_NO_TENSOR, *ok, *ov, *_NO_TENSOR, *_NO_SF, *_NO_SF, B, 0, 0, Hkv, D, room, lens, 0, *out_table, 0.0, 0)
         if (weights is None) != (weights_out is None):
             raise ValueError("weights and weights_out go together")
-    w = wo = 0
-    nw = nwo = 0
+    w = wo = nw = nwo = 0
     if weights is not None:
         if weights.dim() != 3 or (weights_out is not None and weights_out.dim() != 3):
             raise ValueError("weights must be contiguous float32 [B, Hkv, n] tensors")
-        w, nw = _floats(weights, (B, Hkv, weights.shape[2]), "weights"), weights.shape[2]
+        nw = weights.shape[2]
+        w = _array(weights, torch.float32, (B, Hkv, nw), "weights")
         wo, nwo = w, nw
         if weights_out is not None:
-            wo, nwo = _floats(weights_out, (B, Hkv, weights_out.shape[2]), "weights_out"), weights_out.shape[2]
+            nwo = weights_out.shape[2]
+            wo = _array(weights_out, torch.float32, (B, Hkv, nwo), "weights_out")
+    _int32s("n", shape[2], nw, nwo)
     lib = load_library()
     with _launch(stream, k, v, keep, counts, dst_start, page_table, k_out, v_out, out_page_table, weights,
                  weights_out) as s:
-        _check(lib.fmha_cache_compact(a, o, keep.data_ptr(),
-                                      keep.stride(0) if B > 1 else 0, keep.stride(1) if keep.shape[1] > 1 else 0,
-                                      _int32(keep.shape[2], "n_keep"), counts.data_ptr(), start, w,
-                                      _int32(nw, "n"), wo, _int32(nwo, "n"), s))
+        _check(lib.fmha_cache_compact(a, o, keep.data_ptr(), stride[0] if B > 1 else 0, stride[1] if shape[1] > 1 else 0,
+                                      shape[2], lens, start, w, nw, wo, nwo, s))
     return (k, v) if k_out is None else (k_out, v_out)
