@@ -119,33 +119,31 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
     }
     limit = prefix;
   }
-  // Warps take consecutive runs of positions, lanes words of them. A lane reads its word from its own number on, round, so
-  // that the lanes are in different banks (votes over neighbouring keys: 6900 clocks, not 5000). Long runs have words of
-  // 32 (words of run / 32 collide in the banks: 120 us for 8 x 8 heads of 25-33k keys with their move, not 111), short
-  // ones small words (2049 keys on 8 heads: 13.8 us with words of 32, else 11.8).
-  const int run = ((n + kEvictWarps - 1) / kEvictWarps + 31) & ~31, width = run > 256 ? 32 : run / 32;
-  const int step = 32 * width;
+  // Warps take consecutive runs of positions, lanes words of an odd number of them, so that the lanes are in different banks
+  // (votes over neighbouring keys: 6900 clocks, not 5000, for a run of 1024).
+  const int run = ((n + kEvictWarps - 1) / kEvictWarps + 31) & ~31;
+  const int words = (run + 991) / 992, width = (run / 32 + words - 1) / words | 1, step = 32 * width;  // words of a lane
   const int j0 = min(n, warp * run), j1 = min(n, j0 + run);
   auto verdicts = [&](int at, uint32_t& gt, uint32_t& eq) {
     gt = eq = 0u;
     if (at >= j1) return;
-    int x = lane % width;
 #pragma unroll 4  // a short loop: code that runs once waits for its instructions
     for (int i = 0; i < width; ++i) {
-      const uint32_t k = key_of(min(at + x, n - 1));
-      gt |= (k > limit ? 1u : 0u) << x;
-      eq |= (k == limit ? 1u : 0u) << x;
-      x = x + 1 == width ? 0 : x + 1;
+      const uint32_t k = key_of(min(at + i, n - 1));
+      gt |= (k > limit ? 1u : 0u) << i;
+      eq |= (k == limit ? 1u : 0u) << i;
     }
     auto below = [&](int j) { return j <= at ? 0u : j >= at + 32 ? kFull : (1u << (j - at)) - 1u; };
     const uint32_t forced = below(m0) | ~below(m1), live = below(min(j1, at + width));
     gt = (gt | forced) & live;
     eq = eq & ~forced & live;
   };
-  uint32_t gt = 0u, eq = 0u;
+  uint32_t gt = 0u, eq = 0u, kept[2][2] = {{0u, 0u}, {0u, 0u}};
   int gt0 = 0, eq0 = 0;
   for (int j = j0; j < j1; j += step) {
     verdicts(j + width * lane, gt, eq);
+    if (j == j0) kept[0][0] = gt, kept[0][1] = eq;
+    else kept[1][0] = gt, kept[1][1] = eq;
     gt0 += __reduce_add_sync(kFull, __popc(gt));
     eq0 += __reduce_add_sync(kFull, __popc(eq));
   }
@@ -153,11 +151,13 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
   __syncthreads();
   gt0 = __reduce_add_sync(kFull, lane < warp ? warp_gt[lane] : 0);
   eq0 = __reduce_add_sync(kFull, lane < warp ? warp_eq[lane] : 0);
-  // Listed in the keys' place, which have done their work, and written side by side from there.
-  const bool staged = CACHED && run <= step;
-  int32_t* list = staged ? reinterpret_cast<int32_t*>(cached) : keep;
+  // Cached keys have done their work: at most two words a lane hold the verdicts, and the positions are listed in the keys'
+  // place and written side by side from there.
+  static_assert(kEvictCached <= kEvictWarps * 2 * 32 * 31, "two words a lane");
+  int32_t* list = CACHED ? reinterpret_cast<int32_t*>(cached) : keep;
   for (int j = j0; j < j1; j += step) {
-    if (run > step) verdicts(j + width * lane, gt, eq);  // else the words are still here
+    if constexpr (CACHED) gt = kept[j != j0][0], eq = kept[j != j0][1];
+    else verdicts(j + width * lane, gt, eq);
     // Verdicts of the words before: two counts of at most 1024 in one word.
     const uint32_t mine = __popc(gt) | __popc(eq) << 16;
     uint32_t before = mine;
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
     gt0 += static_cast<int>(total & 0xffffu);
     eq0 += static_cast<int>(total >> 16);
   }
-  if (!staged) return;
+  if constexpr (!CACHED) return;
   __syncthreads();
   for (int i = tid; i < count; i += kEvictThreads) keep[i] = list[i];
 }
