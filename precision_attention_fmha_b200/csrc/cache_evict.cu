@@ -24,7 +24,7 @@ constexpr int kEvictThreads = 1024, kEvictWarps = kEvictThreads / 32;
 // (11 + 11 + 10 bits), then the kept positions in ascending order. (Four CTAs a
 // head, joining their counters over distributed shared memory, were slower for
 // 64 heads of 32768 weights, 35 against 27 us: eight cluster barriers.) 20 us
-// for those: a seventh of it the weights' way here, the rest the passes of one
+// for those: a fifth of it the weights' way here, the rest the passes of one
 // SM a head.
 // CACHED: the keys stay in shared memory between the passes.
 constexpr int kEvictCached = 49152;  // keys

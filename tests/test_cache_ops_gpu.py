@@ -179,6 +179,7 @@ def test_weights(B, T, Hq, Hkv, D, lens, page, kv, causal):
     (1, 2, [40000], 7, 0, 0), (2, 1, [3000, 0], 2999, 1, 1), (1, 1, [70], 8, 4, 4),
     (1, 1, [120000], 30001, 16, 100), (3, 8, [9000, 20000, 8193], 8192, 1, 0), (40, 4, [600 + i for i in range(40)], 601, 0, 1),
     (160, 1, [60000] * 160, 100, 1, 1),  # too many keys for shared memory
+    (3, 1, [49149, 31745, 31744], 20000, 3, 5), (2, 1, [32768, 993], 992, 0, 0), (2, 2, [65000, 49153], 48000, 7, 9),
 ])
 def test_evict_select(B, Hkv, lens, budget, sinks, recent):
     from precision_attention_fmha_b200 import fmha
