@@ -46,6 +46,7 @@ def test_bounds(B, Hkv, D, lens, block, page, kv):
     (1, 1, 1, 1, 64, [1], 16, 1, 0, 1), (1, 1, 8, 2, 128, [1000], 16, 5, 1, 2), (2, 3, 12, 4, 64, [700, 90], 32, 4, 0, 0),
     (1, 2, 4, 1, 128, [40000], 16, 64, 2, 3), (1, 1, 2, 2, 64, [120000], 16, 700, 1, 1), (3, 2, 8, 8, 128, [64, 65, 63], 64, 1, 0, 1),
     (2, 1, 4, 2, 128, [5000, 1], 128, 40, 1, 1), (1, 1, 4, 2, 128, [3000], 16, 2, 3, 4),
+    (1, 1, 2, 1, 64, [16384 * 16], 16, 2000, 1, 1),  # the most blocks
 ])
 def test_pick_lists(B, T, Hq, Hkv, D, lens, block, top, sinks, recent):
     from precision_attention_fmha_b200 import fmha
@@ -81,6 +82,35 @@ def test_pick_ties_go_to_the_lowest_block():
     bnd[:] = -1.0
     got = fmha.select_blocks(q, bnd, i32([640]), 16, 4, 0, 0)
     assert got.flatten().tolist() == [0, 1, 2, 3]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_pick_over_the_whole_range_of_values(D):
+    """Queries and bounds of every BF16 magnitude, subnormals and the largest among them, in every channel."""
+    from precision_attention_fmha_b200 import fmha
+
+    g = torch.Generator(device=DEV)
+    g.manual_seed(D + 1)
+
+    def any_bf16(*shape):
+        bits = torch.randint(0, 0x7f80, shape, generator=g, device=DEV) | torch.randint(0, 2, shape, generator=g, device=DEV) << 15
+        return torch.where(bits >= 0x8000, bits - 0x10000, bits).to(torch.int16).view(torch.bfloat16)
+
+    q = any_bf16(2, 2, 6, D)
+    q[1] *= 2.0 ** -100  # one sequence's scores are all tiny
+    x = any_bf16(2, 3, 200, 2, D)
+    x[1] *= 2.0 ** -30
+    bnd = torch.stack([x.amin(3), x.amax(3)], 3)
+    lens = [200 * 16, 150 * 16 + 3]
+    got = fmha.select_blocks(q, bnd, i32(lens), 16, 30, 1, 2)
+    for b, rows in enumerate(ref.pick(q, bnd, lens, 16, 30, 1, 2)):
+        for t, heads in enumerate(rows):
+            for h, ids in enumerate(heads):
+                assert got[b, t, h].tolist() == ids
+    tiny = torch.full((1, 1, 1, D), 2.0 ** -133, device=DEV).bfloat16()  # the smallest of all
+    low = torch.zeros(1, 1, 9, 2, D, device=DEV).bfloat16()
+    low[0, 0, 4, 1, D - 1] = low[0, 0, 6, 1, 2] = 2.0 ** -133
+    assert fmha.select_blocks(tiny, low, i32([9 * 16]), 16, 2, 0, 0).flatten().tolist() == [4, 6]
 
 
 @pytest.mark.parametrize("D", [64, 128])
