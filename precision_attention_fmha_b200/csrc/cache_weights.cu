@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(KmCfg<D>::THREADS, 2)
   for (int turn = 0;; ++turn) {
     // Items in order: the first keys are seen by the most queries and start first.
     const uint32_t item = misc->item[turn & 1];
-    if (item >= p.n_items || misc->abort) break;
+    if (item >= p.n_items) break;
     const Item x = decode(item);
     const int part = x.part, bh = x.bh, b = x.b, hkv = x.hkv, key0 = x.key0, n_keys = x.n_keys, base = x.base, tt0 = x.tt0;
     const int it0 = x.it0, n_it = x.n_it;
@@ -435,7 +435,11 @@ __global__ void __launch_bounds__(KmCfg<D>::THREADS, 2)
       }
     }
     cnt += max(0, n_it);
-    __syncthreads();  // every product that reads the keys is done, and the next item is there
+    // Every product that reads the keys is done, and the next item is there. A wait that ran out ends the loop, for all
+    // threads after the same turn: whoever raised the flag did so before it came here, and the barrier carries it. (Each
+    // thread's own look at the flag after the barrier could see what a faster warp raised in the next turn already, and
+    // the named barriers above would then wait for warps that have left.)
+    if (__syncthreads_or(misc->abort != 0u)) break;
   }
   // Every copy and product issued has ended before shared and tensor memory go away (after an abort some may be in flight).
   if (warp == C::LOAD_WARP && lane == 0)

@@ -397,3 +397,29 @@ def test_wait_that_runs_out_is_reported():
         assert e.value.status == fmha.FMHA_ERR_TIMEOUT
     assert torch.equal(fmha.fmha_fwd_tree(q, k, v, lens), want)
     fmha.get_device_error()
+
+
+@pytest.mark.parametrize("cycles", [1, 300, 1000, 3000, 10000, 100000])
+def test_weights_whose_waits_run_out_in_any_turn(cycles):
+    """A prompt's weights take each CTA through many turns: whichever turn's wait runs out, first or later, all warps leave
+    after the same one; the call returns, says so if a wait ran out, and the next call is whole."""
+    from precision_attention_fmha_b200 import fmha
+
+    B, T, Hq, Hkv, D, n = 2, 1500, 8, 2, 64, 4000
+    q, k, v, _, g = make(12, B, T, Hq, Hkv, D, n)
+    lens, lse = i32([n, n - 9]), torch.full((B, Hq, T), 8.0, device=DEV)
+    want = fmha.key_weights(q, k, lse, torch.zeros(B, Hkv, n, device=DEV), lens)
+    fmha.get_device_error()
+    for _ in range(5):
+        fmha.set_wait_timeout_cycles(cycles)
+        try:
+            fmha.key_weights(q, k, lse, torch.zeros(B, Hkv, n, device=DEV), lens)
+            torch.cuda.synchronize()
+        finally:
+            fmha.set_wait_timeout_cycles(0)
+        try:
+            fmha.get_device_error()
+        except fmha.FmhaError as e:
+            assert e.status == fmha.FMHA_ERR_TIMEOUT
+        assert torch.equal(fmha.key_weights(q, k, lse, torch.zeros(B, Hkv, n, device=DEV), lens), want)
+    fmha.get_device_error()
