@@ -327,6 +327,9 @@ __device__ void produce(const CacheParams& p, uint8_t* ring, RingMisc<C::STAGES>
       const bool live = __shfl_sync(kFull, cur.valid, src) > 0 && my_piece < ppt;
       const uint32_t n = __popc(__ballot_sync(kFull, live && my_copy == 0));
       const uint32_t full = smem_addr(&misc->full[s]);
+      // Lane 0's arrival publishes what all four lanes wrote to meta[s] (votes and shuffles do not order memory); a tile
+      // without a live piece is full at once, so no copy's latency would cover for it.
+      __syncwarp();
       if (lane == 0) mbar_arrive_expect_tx(full, (n << ps) * (C::KL::ROW + (C::HAS_V ? C::VL::ROW : 0)));
       __syncwarp();
       if (live) {

@@ -228,3 +228,27 @@ def test_zero_scale(T):
     ids = torch.tensor([0, 3, 2, 7], dtype=torch.int32, device=DEV).expand(2, T, 2, 4).contiguous()
     o = fmha.fmha_fwd_selected(q, k, v, ids, i32(lens), 16, sf_k=sk, sf_v=sv, lse=lse)
     ref.check(o, lse, ref.selected(q, k, v, ids, lens, 16, None, None, sk, sv), v8=True)
+
+
+@pytest.mark.parametrize("Hq,kv", [(4, "bf16"), (40, "bf16"), (4, "e4m3")])
+def test_selected_with_tiles_that_hold_no_block(Hq, kv):
+    """Lists with gaps of whole 64-key tiles between their blocks: an empty tile is full at once, and must hide its slot."""
+    from precision_attention_fmha_b200 import fmha
+
+    B, T, Hkv, D, lens, block, top = 3, 4, 2, 64, [3000, 64, 1501], 64, 40
+    q, k, v, sf, g = make(31, B, T, Hq, Hkv, D, max(lens) + 3, 0, kv)
+    poison(k, lens), poison(v, lens)
+    blocks = torch.full((B, T, Hkv, top), -1, dtype=torch.int32, device=DEV)
+    for b in range(B):
+        nb = -(-lens[b] // block)
+        for t in range(T):
+            for h in range(Hkv):
+                n = min(nb, (5 * t + 3 * h + b) % 18)
+                at = torch.randperm(top, generator=g, device=DEV)[:n]
+                blocks[b, t, h, at] = torch.randperm(nb, generator=g, device=DEV)[:n].to(torch.int32)
+    lse = torch.empty(B, Hq, T, device=DEV)
+    o = fmha.fmha_fwd_selected(q, k, v, blocks, i32(lens), block, sf_k=sf[0], sf_v=sf[1], lse=lse)
+    fmha.get_device_error()
+    ref.check(o, lse, ref.selected(q, k, v, blocks, lens, block, None, None, *sf), v8=kv != "bf16")
+    for _ in range(50):
+        assert torch.equal(fmha.fmha_fwd_selected(q, k, v, blocks, i32(lens), block, sf_k=sf[0], sf_v=sf[1]), o)
