@@ -1284,7 +1284,10 @@ __device__ void attn_softmax_role(const AttnParams& p, const TileInfo t, int x, 
   }
   float sfv = 1.f;
   if (C::PV == PV_E4M3 && p.sf_v_kind != FMHA_SF_PER_CHANNEL) sfv = sf_lookup(p.sf_v, p.sf_v_kind, bhk, 1, 0, 1);
-  const float inv_l = l > 0.f ? sfv / l : 0.f;
+  // A row that saw keys. Ragged parts are joined by their log-sum-exps, -inf for no key: there a NaN sum (a NaN score) has
+  // to stay one and give a NaN part, or the join would drop the part's keys.
+  const bool any = C::RAGGED ? l != 0.f : l > 0.f;
+  const float inv_l = any ? sfv / l : 0.f;
   const uint32_t stage0 = smem_addr(sQx);
   constexpr uint32_t TILE_THREADS = 128;
   if constexpr (C::SPLIT) {
@@ -1446,7 +1449,7 @@ __device__ void attn_softmax_role(const AttnParams& p, const TileInfo t, int x, 
       bulk_commit();
     }
   }
-  const float lse = l > 0.f ? (m + __log2f(l) - log2g) * 0.69314718055994531f : -INFINITY;
+  const float lse = any ? (m + __log2f(l) - log2g) * 0.69314718055994531f : -INFINITY;
   if (C::PACKED && p.n_parts > 1) {
     if (row < p.Sq && ok) p.lse_part[(((int64_t)t.part * p.B + b) * p.Hq + head) * p.Sq + row] = lse;
   } else if (p.lse != nullptr && row < p.Sq && ok) {

@@ -1,0 +1,64 @@
+"""The operators over a ragged cache at their edges: many-row trees (contexts on the packed tensor-memory tiles) with
+non-finite keys, bad lengths and pages, strides and many sequences; long flat tails; empty groups of queries."""
+
+import math
+
+import pytest
+import torch
+
+import cache_ref as ref
+from test_cache_attn_gpu import DEV, i32, make, poison, random_tree, to_pages
+
+pytestmark = pytest.mark.gpu
+
+PACKED = [
+    # B, T, Hq, Hkv, room, page
+    (1, 16, 16, 2, 1300, 0),    # 128 rows (two tiles of the same rows take alternate keys), one split
+    (1, 16, 16, 2, 3300, 64),   # several splits
+    (1, 40, 16, 2, 1300, 16),   # 320 rows
+    (1, 40, 16, 2, 3300, 0),
+    (10, 5, 64, 8, 1300, 0),    # 40 rows on many heads
+    (10, 5, 64, 8, 2500, 128),
+]
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,room,page", PACKED)
+@pytest.mark.parametrize("bad", ["k nan", "k inf", "v nan"])
+@pytest.mark.parametrize("where", ["middle", "last"])
+def test_packed_non_finite_context(B, T, Hq, Hkv, room, page, bad, where):
+    """A key of the context whose score is NaN makes every row of its KV head NaN, as in the few-row kernel, whatever tile
+    or split it is in; a NaN value its column. All other rows keep their bits."""
+    from precision_attention_fmha_b200 import fmha
+
+    D, G = 128, Hq // Hkv
+    ctx = [room - T - 20 - 7 * b for b in range(B)]
+    q, k, v, _, g = make(41, B, T, Hq, Hkv, D, room, page)
+    at = 3 * 128 + 5 if where == "middle" else ctx[-1] // 128 * 128 - 1
+    x, y = k.clone(), v.clone()
+    if bad == "v nan":
+        y[-1, at, -1, 7] = float("nan")
+    else:
+        x[-1, at, -1, 3] = float("nan" if bad == "k nan" else "inf")
+
+    def run(k, v):
+        table = None
+        if page:
+            k, v, table = to_pages(k, v, page, torch.Generator(device=DEV).manual_seed(1))
+        lse = torch.empty(B, Hq, T, device=DEV)
+        return fmha.fmha_fwd_tree(q, k, v, i32(ctx), None, None, table, lse=lse), lse
+
+    want, want_lse = run(k, v)
+    o, lse = run(x, y)
+    fmha.get_device_error()
+    assert torch.isfinite(want).all() and torch.isfinite(want_lse).all()
+    heads = slice(Hq - G, Hq)  # of the last KV head
+    if bad == "v nan":
+        assert torch.isnan(o[-1, :, heads, 7]).all()
+        o[-1, :, heads, 7] = want[-1, :, heads, 7]
+    else:
+        hit = (q[-1, :, heads, 3] >= 0) if bad == "k inf" else torch.ones(T, G, dtype=torch.bool, device=DEV)
+        assert torch.equal(torch.isnan(o[-1, :, heads]).all(-1), hit)
+        assert torch.equal(~torch.isfinite(lse[-1, heads]).t(), hit)
+        assert torch.equal(torch.isfinite(o[-1, :, heads]).all(-1), ~hit)
+        o[-1, :, heads], lse[-1, heads] = want[-1, :, heads], want_lse[-1, heads]
+    assert torch.equal(o, want) and torch.equal(lse, want_lse)
