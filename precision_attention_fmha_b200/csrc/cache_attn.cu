@@ -53,6 +53,12 @@ struct CaCfg {
   static constexpr int RED_BYTES = 4 * 16 * RED_LD * 4;
   static constexpr int SMEM = STAGES * SLOT + RED_BYTES + 2048;
   static constexpr int THREADS = 160;
+  // The running maximum of the transposed arrangement moves when it is exceeded by more than 2^TAU; weights are taken
+  // 2^LIFT above it. BF16 weights have the range of 32 bits. F16 weights (E4M3 values) end at 2^16, are normal down to
+  // 2^-14 and zero below 2^-25: lifted to the top of that range, they are normal down to 2^-28 of the maximum (2^-29 where
+  // it is exact), so a long flat tail below one dominant key keeps its share. Without, 65536 keys of 2^-27 were lost.
+  static constexpr float TAU = V8 ? 1.875f : 8.f;
+  static constexpr float LIFT = !V8 ? 0.f : NT ? 14.f : 15.f;
 };
 
 template <int STAGES>
@@ -252,7 +258,7 @@ __device__ void consume(const CacheAttnParams& p, uint8_t* ring, float* red, CaM
           for (int i = 0; i < GPW * 2; ++i) mx = fmaxf(mx, fmaxf(sc[i][2 * h], sc[i][2 * h + 1]));
           mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-          const float mn = fmaxf(m[h], mx * cs[h]);
+          const float mn = fmaxf(m[h], mx * cs[h] - C::LIFT);  // m: 2^LIFT below the maximum
           const bool up = mn > m[h];
           if (__any_sync(kFull, up)) {
             const float f = up ? ex2(m[h] - mn) : 1.f;
@@ -576,7 +582,6 @@ template <class C>
 __device__ void consume_t(const CacheAttnParams& p, uint8_t* ring, float* red, CaMisc<C::STAGES>* misc, const Waiter w) {
   using namespace ptx;
   constexpr int D = C::D, KS = D / 16, NQ = D / 32, NT = C::NT;
-  constexpr float kTau = 8.f;  // the running maximum moves when it is exceeded by more than 2^8 (weights stay below it)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gq = lane >> 2, j = lane & 3;
   uint32_t it = 0;
@@ -680,7 +685,7 @@ __device__ void consume_t(const CacheAttnParams& p, uint8_t* ring, float* red, C
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) over = over || fmaxf(sc[n][e], sc[n][2 + e]) * cs[n][e] > m[n][e] + kTau;
+          for (int e = 0; e < 2; ++e) over = over || fmaxf(sc[n][e], sc[n][2 + e]) * cs[n][e] > m[n][e] + (C::TAU + C::LIFT);
         if (__any_sync(kFull, over)) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
@@ -690,7 +695,7 @@ __device__ void consume_t(const CacheAttnParams& p, uint8_t* ring, float* red, C
               mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
               mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
               mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
-              const float mn = fmaxf(m[n][e], mx);
+              const float mn = fmaxf(m[n][e], mx - C::LIFT);  // m: 2^LIFT below the maximum
               const float f = mn > m[n][e] ? ex2(m[n][e] - mn) : 1.f;
               m[n][e] = mn;
               l[n][e] *= f;

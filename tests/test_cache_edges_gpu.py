@@ -62,3 +62,36 @@ def test_packed_non_finite_context(B, T, Hq, Hkv, room, page, bad, where):
         assert torch.equal(torch.isfinite(o[-1, :, heads]).all(-1), ~hit)
         o[-1, :, heads], lse[-1, heads] = want[-1, :, heads], want_lse[-1, heads]
     assert torch.equal(o, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "bf16_e4m3", "e4m3"])
+@pytest.mark.parametrize("Hq", [8, 16, 32, 64])  # rows a KV head: every arrangement of the few-row kernel
+def test_long_flat_tail(Hq, kv):
+    """One dominant key, then 65536 keys of 2^-27 of its weight each: what they add up to (2^-11) is neither lost nor
+    skewed by the 16-bit weights. All sequences read the same pages, and there are enough for a CTA to walk a sequence
+    whole. Lifted as
+    they are, all 16-bit weights are normal numbers, so the tolerance is that of cache_ref.check (A = O: no value is negative);
+    the tail's weights are equal, and the 32-bit sums of 2^14 of them per warp and column are off by 2^-24 * 2^14 / 16
+    relative at the worst (one addition per 16 keys), 2^-14, which 2^-12 A holds beside the rest."""
+    from precision_attention_fmha_b200 import fmha
+
+    B, D, page, N = 444, 64, 128, 65536
+    wide = N // page + 1
+    kt = torch.float8_e4m3fn if kv == "e4m3" else torch.bfloat16
+    vt = torch.bfloat16 if kv == "bf16" else torch.float8_e4m3fn
+    k, v = torch.zeros(wide, page, 1, D, device=DEV), torch.zeros(wide, page, 1, D, device=DEV)
+    k[0, 0, 0, 0] = 12.0
+    v[..., :32] = 1.0  # the tail's columns
+    v[0, 0, 0, :32], v[0, 0, 0, 32:] = 0.0, 1.0
+    q = torch.zeros(B, 1, Hq, D, device=DEV, dtype=torch.bfloat16)
+    q[..., 0] = 12.5
+    table = torch.arange(wide, device=DEV, dtype=torch.int32).expand(B, wide).contiguous()
+    lse = torch.empty(B, Hq, 1, device=DEV)
+    o = fmha.fmha_fwd_tree(q, k.to(kt), v.to(vt), i32([N] * B), page_table=table, lse=lse)
+    fmha.get_device_error()
+    z = 12.5 * 12.0 / 8.0
+    tail = N * math.exp(-z)  # the node is the last of the N keys behind the first
+    want = torch.full((D,), tail / (1 + tail), dtype=torch.float64, device=DEV)
+    want[32:] = 1 / (1 + tail)
+    ref.check(o, lse, (want.expand(B, 1, Hq, D), torch.full((B, Hq, 1), z + math.log1p(tail), dtype=torch.float64, device=DEV),
+                       want.expand(B, 1, Hq, D)), v8=kv != "bf16")
