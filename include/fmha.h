@@ -443,7 +443,8 @@ fmha_status fmha_select_blocks(const fmha_cache_args* args, const void* bounds, 
  * log-sum-exp that an attention call on the same q and keys wrote.
  *   Reads q, k, lse, lens, q_lens and sf_k of args.
  *   weights: fp32 [B, Hkv, n_weights] contiguous, device; accumulate != 0 adds,
- *     0 overwrites. Entries at or past lens[b] are left as they were;
+ *     0 overwrites (without query tokens or heads with zeros). Entries at or
+ *     past lens[b] are left as they were;
  *     lens[b] <= n_weights. The same inputs give the same bits.
  *   workspace: device, 16-byte aligned, caller-owned, at least
  *     fmha_key_weights_workspace_bytes(args, n_weights, causal) bytes (0, and

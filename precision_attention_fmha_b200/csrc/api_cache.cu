@@ -518,16 +518,25 @@ fmha_status fmha_key_weights(const fmha_cache_args* a, float* weights, int32_t n
                              int32_t accumulate, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   if (a == nullptr) return fail(FMHA_ERR_INVALID_ARG, "args is NULL");
   if (!sizes_ok(a) || n_weights < 0) return fail(FMHA_ERR_INVALID_ARG, "negative size");
-  if (a->B == 0 || a->T == 0 || a->Hq == 0 || n_weights == 0) return ok_status();
+  const bool no_rows = a->T == 0 || a->Hq == 0;  // every sum is empty
+  if (a->B == 0 || n_weights == 0 || (no_rows && (accumulate != 0 || a->Hkv == 0))) return ok_status();
   if (weights == nullptr || (reinterpret_cast<uintptr_t>(weights) & 3u))
     return fail(FMHA_ERR_INVALID_ARG, "weights is NULL or misaligned");
-  if (a->lse == nullptr) return fail(FMHA_ERR_INVALID_ARG, "lse is NULL");
+  if (a->lse == nullptr && !no_rows) return fail(FMHA_ERR_INVALID_ARG, "lse is NULL");
   KeyWeightsParams p;
   memset(&p, 0, sizeof(p));
   bool k8, v8;
   fmha_status st;
-  if ((st = check_cache(a, true, false, &p.c, &k8, &v8)) != FMHA_OK) return st;
+  if ((st = check_cache(a, !no_rows, false, &p.c, &k8, &v8)) != FMHA_OK) return st;
   if (p.c.capacity == 0) return ok_status();  // no key
+  if (no_rows) {
+    if ((st = bind_device(&p.c)) != FMHA_OK) return st;
+    p.weights = weights;
+    p.n_weights = n_weights;
+    const cudaError_t e = launch_key_weights_clear(p, stream);
+    if (e != cudaSuccess) return fail(FMHA_ERR_CUDA, "key weights launch: %s", cudaGetErrorString(e));
+    return ok_status();
+  }
   p.q = static_cast<const uint16_t*>(a->q.ptr);
   p.q_sb = a->q.stride_b; p.q_ss = a->q.stride_s; p.q_sh = a->q.stride_h;
   p.k = static_cast<const uint8_t*>(a->k.ptr);

@@ -75,6 +75,8 @@ struct KeyWeightsParams : CacheParams {
 // tq: TMA map of q (boxes of 128 tokens of one head); tk: of k (64-key ring tiles).
 cudaError_t launch_key_weights_few(int D, bool k8, const KeyWeightsParams& p, const CUtensorMap& tk, cudaStream_t s);
 cudaError_t launch_key_weights_many(int D, bool k8, const KeyWeightsParams& p, const CUtensorMap& tq, cudaStream_t s);
+// Without query rows: weights[b, h, s] = 0 for every key s of sequence b.
+cudaError_t launch_key_weights_clear(const KeyWeightsParams& p, cudaStream_t s);
 
 // Keys that stay in a cache under a budget.
 struct EvictParams {

@@ -472,6 +472,21 @@ __global__ void __launch_bounds__(256) key_weights_join_kernel(const __grid_cons
   p.weights[at] = sum;
 }
 
+// The sums of a call without query rows, 1024 keys of one (sequence, KV head) at a time.
+constexpr int kClearKeys = 1024;
+__global__ void __launch_bounds__(256) key_weights_clear_kernel(const __grid_constant__ KeyWeightsParams p, long long items) {
+  const long long heads = static_cast<long long>(p.c.B) * p.c.Hkv;
+  for (long long item = blockIdx.x; item < items; item += gridDim.x) {
+    const long long run = item / heads, bh = item - run * heads;
+    const int b = static_cast<int>(bh / p.c.Hkv);
+    bool bad;
+    const SeqLens s = seq_lens(p.c, b, bad);
+    if (threadIdx.x == 0 && run == 0 && bh % p.c.Hkv == 0 && (bad || s.len > p.n_weights)) atomicOr(p.c.err, kErrLength);
+    const int first = static_cast<int>(run) * kClearKeys, end = min(first + kClearKeys, min(s.len, p.n_weights));
+    for (int key = first + threadIdx.x; key < end; key += 256) p.weights[bh * p.n_weights + key] = 0.f;
+  }
+}
+
 template <class C>
 cudaError_t launch_few(const KeyWeightsParams& p, const CUtensorMap& tk, cudaStream_t s) {
   auto kern = key_weights_few_kernel<C>;
@@ -504,6 +519,11 @@ cudaError_t launch_many(const KeyWeightsParams& p, const CUtensorMap& tq, cudaSt
 
 }  // namespace
 
+cudaError_t launch_key_weights_clear(const KeyWeightsParams& p, cudaStream_t s) {
+  const long long items = static_cast<long long>(p.c.B) * p.c.Hkv * ((std::min(p.c.capacity, p.n_weights) + kClearKeys - 1LL) / kClearKeys);
+  key_weights_clear_kernel<<<static_cast<unsigned>(std::min(items, 1LL << 20)), 256, 0, s>>>(p, items);
+  return cudaGetLastError();
+}
 cudaError_t launch_key_weights_few(int D, bool k8, const KeyWeightsParams& p, const CUtensorMap& tk, cudaStream_t s) {
   if (D == 64) return k8 ? launch_few<KwCfg<64, true>>(p, tk, s) : launch_few<KwCfg<64, false>>(p, tk, s);
   return k8 ? launch_few<KwCfg<128, true>>(p, tk, s) : launch_few<KwCfg<128, false>>(p, tk, s);

@@ -95,3 +95,31 @@ def test_long_flat_tail(Hq, kv):
     want[32:] = 1 / (1 + tail)
     ref.check(o, lse, (want.expand(B, 1, Hq, D), torch.full((B, Hq, 1), z + math.log1p(tail), dtype=torch.float64, device=DEV),
                        want.expand(B, 1, Hq, D)), v8=kv != "bf16")
+
+
+@pytest.mark.parametrize("T,Hq", [(0, 4), (3, 0), (0, 0)])
+@pytest.mark.parametrize("page", [0, 16])
+def test_weights_without_query_rows(T, Hq, page):
+    """An empty sum is zero: written over what the weights held up to each length, or added to it."""
+    from precision_attention_fmha_b200 import fmha
+
+    B, Hkv, D, lens = 3, 2, 64, [1500, 0, 33]
+    _, k, v, _, g = make(51, B, 1, 2, Hkv, D, 1504, page)
+    table = None
+    if page:
+        k, v, table = to_pages(k, v, page, g)
+    q = torch.empty(B, T, Hq, D, device=DEV, dtype=torch.bfloat16)
+    w0 = torch.rand(B, Hkv, 1501, generator=g, device=DEV)
+    want = w0.clone()
+    for b, n in enumerate(lens):
+        want[b, :, :n] = 0
+    lse = torch.empty(B, Hq, T, device=DEV)
+    assert torch.equal(fmha.key_weights(q, k, lse, w0.clone(), i32(lens), page_table=table, accumulate=False), want)
+    assert torch.equal(fmha.key_weights(q, k, lse, w0.clone(), i32(lens), page_table=table, accumulate=True), w0)
+    fmha.get_device_error()
+    far = [1505, -1, 33]
+    want[0, :, 1500] = 0
+    assert torch.equal(fmha.key_weights(q, k, lse, w0.clone(), i32(far), page_table=table, accumulate=False), want)
+    with pytest.raises(fmha.FmhaError) as e:
+        fmha.get_device_error()
+    assert e.value.status == fmha.FMHA_ERR_DEVICE_INDEX

@@ -232,3 +232,16 @@ def test_numbers_that_32_bits_do_not_hold():
               lambda: fmha.key_bounds(k, lens, 16, page_table=torch.empty(1, 1 << 25, dtype=torch.int32))):
         with pytest.raises(ValueError, match="out of range"):
             f()
+
+
+@pytest.mark.parametrize("empty", ["T", "Hq"])
+def test_weights_without_query_rows_refuse(lib, empty):
+    """Sums over no query row are written where they overwrite: what is written to and the cache are checked all the same."""
+    def call(w=P, accumulate=0, **kw):
+        a = cache()
+        set_(a, **{empty: 0, **kw})
+        a.q.ptr = None
+        return lib.fmha_key_weights(ctypes.byref(a), w, 320, 1, accumulate, None, 0, None)
+
+    assert call(accumulate=1) == 0 and call(B=0) == 0 and call(**{"Hq": 0, "Hkv": 0}) == 0
+    assert call(w=None) == 1 and call(w=P + 2) == 1 and call(lens=None) == 1 and call(D=96) == 2 and call(page_size=48) == 2
