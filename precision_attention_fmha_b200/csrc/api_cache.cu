@@ -459,7 +459,8 @@ fmha_status fmha_select_blocks(const fmha_cache_args* a, const void* bounds, int
                                cudaStream_t stream) {
   if (a == nullptr) return fail(FMHA_ERR_INVALID_ARG, "args is NULL");
   if (!sizes_ok(a) || n_blocks < 0) return fail(FMHA_ERR_INVALID_ARG, "negative size");
-  if (a->B == 0 || a->T == 0 || a->Hq == 0) return ok_status();
+  // Without query heads the scores are empty sums, and the ties' rule picks.
+  if (a->B == 0 || a->T == 0 || (a->Hq == 0 && a->Hkv == 0)) return ok_status();
   fmha_status st;
   if ((st = check_block(block)) != FMHA_OK) return st;
   if (top <= 0) return fail(FMHA_ERR_INVALID_ARG, "top must be positive");
@@ -471,7 +472,7 @@ fmha_status fmha_select_blocks(const fmha_cache_args* a, const void* bounds, int
   if (a->Hkv == 0 || a->Hq % a->Hkv != 0)
     return fail(FMHA_ERR_INVALID_ARG, "Hq (%d) must be a multiple of Hkv (%d)", a->Hq, a->Hkv);
   if (a->q.dtype != FMHA_BF16) return fail(FMHA_ERR_UNSUPPORTED, "q must be BF16");
-  if ((st = check_tensor(a->q, "q", a->B, a->T, a->Hq, a->D)) != FMHA_OK) return st;
+  if (a->Hq > 0 && (st = check_tensor(a->q, "q", a->B, a->T, a->Hq, a->D)) != FMHA_OK) return st;
   if (n_blocks > 0 && (bounds == nullptr || !aligned16(bounds)))
     return fail(FMHA_ERR_INVALID_ARG, "bounds is NULL or not 16-byte aligned");
   if (q_tile == 128 && n_blocks == 0) return ok_status();  // an empty mask

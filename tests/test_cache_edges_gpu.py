@@ -123,3 +123,26 @@ def test_weights_without_query_rows(T, Hq, page):
     with pytest.raises(fmha.FmhaError) as e:
         fmha.get_device_error()
     assert e.value.status == fmha.FMHA_ERR_DEVICE_INDEX
+
+
+@pytest.mark.parametrize("q_tile", [1, 128])
+def test_picks_without_query_heads(q_tile):
+    """No query head: every score is an empty sum, so the ties' rule picks, and the whole of `picked` is written."""
+    from precision_attention_fmha_b200 import fmha
+
+    B, T, Hkv, D, lens, block, top, sinks, recent = 2, 130, 2, 64, [1100, 140], 128, 4, 1, 1
+    q = torch.empty(B, T, 0, D, device=DEV, dtype=torch.bfloat16)
+    nb = 9
+    bnd = torch.randn(B, Hkv, nb, 2, D, device=DEV).bfloat16()
+    shape, dtype = ((B, T, Hkv, top), torch.int32) if q_tile == 1 else ((B, Hkv, 2, nb), torch.uint8)
+    got = fmha.select_blocks(q, bnd, i32(lens), block, top, sinks, recent, q_tile=q_tile, out=torch.full(shape, 99, device=DEV).to(dtype))
+    fmha.get_device_error()
+    want = torch.full(shape, -1 if q_tile == 1 else 0, device=DEV).to(dtype)
+    for b, rows in enumerate(ref.pick(q, bnd, lens, block, top, sinks, recent, None, q_tile)):
+        for i, heads in enumerate(rows):
+            for h, ids in enumerate(heads):
+                if q_tile == 1:
+                    want[b, i, h, : len(ids)] = i32(ids)
+                else:
+                    want[b, h, i, ids] = 1
+    assert torch.equal(got, want)
