@@ -556,6 +556,8 @@ def _scratch(workspace, need, q):
         workspace = q.new_empty(need, dtype=torch.uint8)
     elif workspace.get_device() != q.get_device():
         raise ValueError(f"workspace on {workspace.device}, tensors on {q.device}")
+    elif not workspace.is_contiguous():  # an expanded one claims more bytes than it has
+        raise ValueError("workspace must be contiguous")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 

@@ -245,3 +245,13 @@ def test_weights_without_query_rows_refuse(lib, empty):
 
     assert call(accumulate=1) == 0 and call(B=0) == 0 and call(**{"Hq": 0, "Hkv": 0}) == 0
     assert call(w=None) == 1 and call(w=P + 2) == 1 and call(lens=None) == 1 and call(D=96) == 2 and call(page_size=48) == 2
+
+
+def test_scattered_workspaces_are_refused():
+    """A workspace's bytes are counted from its elements: one whose elements repeat or lie apart is none of that size."""
+    q = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16)
+    whole = torch.empty(256, dtype=torch.float32)
+    assert fmha._scratch(whole, 1024, q)[1:] == (whole.data_ptr(), 1024)
+    for w in (torch.empty(1, dtype=torch.uint8).expand(1024), whole[::2], whole.view(16, 16).t()):
+        with pytest.raises(ValueError, match="contiguous"):
+            fmha._scratch(w, 16, q)
