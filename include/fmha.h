@@ -481,8 +481,8 @@ fmha_status fmha_evict_select(const fmha_cache_args* args, const float* weights,
  *     is NULL): fp32 [B, Hkv, n_weights] / [B, Hkv, n_weights_out]; entries of
  *     weights_out past the moved ones become 0.
  * Rows that are not written to keep what they held. A position out of range,
- * or (out NULL) out of order, is left out and reported as
- * FMHA_ERR_DEVICE_INDEX.                                                     */
+ * or on a bad page, or (out NULL) out of order, is left out, its weight with
+ * it, and reported as FMHA_ERR_DEVICE_INDEX.                                                     */
 fmha_status fmha_cache_compact(const fmha_cache_args* args, const fmha_cache_args* out, const int32_t* keep,
                                int64_t keep_stride_b, int64_t keep_stride_h, int32_t n_keep, const int32_t* counts,
                                const int32_t* dst_start, const float* weights, int32_t n_weights, float* weights_out,

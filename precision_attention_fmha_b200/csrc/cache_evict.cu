@@ -304,7 +304,6 @@ __global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const __grid
   const int tid = threadIdx.x;
   if (what == cols + cols_v) {
     float* w = p.weights_out + static_cast<int64_t>(bh) * p.n_weights_out;
-    const int32_t* keep = p.keep + b * p.keep_sb + h * p.keep_sh;
     for (int r0 = 0; r0 < count; r0 += kMoveThreads * kMoveUnits) {
       float x[kMoveUnits];
       int to[kMoveUnits];
@@ -313,8 +312,9 @@ __global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const __grid
         const int i = r0 + u * kMoveThreads + tid;
         to[u] = -1;
         if (i >= count) continue;
-        const int from = __ldg(keep + i);
-        if (from < start + i || start + i < 0 || (i > 0 && __ldg(keep + i - 1) >= from)) continue;  // reported with the rows
+        Place src, dst;
+        int from;
+        if (!kept_row(p, b, h, i, start, src, dst, from)) continue;  // a row that is left out leaves its weight
         if (start + i >= p.n_weights_out) continue;
         to[u] = start + i;
         x[u] = from < p.n_weights_out ? w[from] : 0.f;

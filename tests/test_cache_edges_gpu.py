@@ -146,3 +146,38 @@ def test_picks_without_query_heads(q_tile):
                 else:
                     want[b, h, i, ids] = 1
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("inside", [True, False])
+@pytest.mark.parametrize("page", [0, 16])
+def test_compact_leaves_out_a_row_with_its_weight(inside, page):
+    """A position past the cache, out of order or on a bad page is reported, and its row and its weight stay as they were."""
+    from precision_attention_fmha_b200 import fmha
+
+    Hkv, D, n, room = 2, 64, 96, 64
+    _, k, v, _, g = make(61, 1, 1, 2, Hkv, D, room, page)
+    table = None
+    if page:
+        k, v, table = to_pages(k, v, page, g)
+        bad = table.clone()
+        bad[0, 2] = 1 << 20  # positions 32..47
+    keep = i32([[[0, 2, 9, 8, 20, 35, 40, 50, 63, 70, 80]]])  # 8: out of order (inside one cache); 70, 80: past the cache
+    count, start = 10, 0
+    w = torch.rand(1, Hkv, n, generator=g, device=DEV)
+    ko, vo = (k, v) if inside else (torch.ones(1, 16, Hkv, D, device=DEV).bfloat16(), torch.ones(1, 16, Hkv, D, device=DEV).bfloat16())
+    wo = w if inside else torch.full((1, Hkv, 14), 5.0, device=DEV)
+    left_out = {9} | ({3} if inside else set()) | ({5, 6} if page else set())
+    want_w, rows_k = wo.clone(), (ref.gather(ko, table, 0, room) if inside else ko[0]).clone()
+    src = ref.gather(k, table, 0, room)
+    for i in range(count):
+        if i not in left_out:
+            want_w[0, :, start + i] = w[0, :, int(keep[0, 0, i])]
+            rows_k[start + i] = src[int(keep[0, 0, i])]
+    want_w[0, :, start + count:] = 0
+    fmha.cache_compact(k, v, keep, i32([count]), page_table=bad if page else None, weights=w,
+                       **({} if inside else dict(k_out=ko, v_out=vo, weights_out=wo)))
+    with pytest.raises(fmha.FmhaError) as e:
+        fmha.get_device_error()
+    assert e.value.status == fmha.FMHA_ERR_DEVICE_INDEX
+    assert torch.equal(ref.gather(ko, table, 0, room) if inside else ko[0], rows_k)
+    assert torch.equal(wo, want_w)
