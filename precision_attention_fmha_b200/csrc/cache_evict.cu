@@ -227,6 +227,12 @@ __device__ __forceinline__ int kept_count(const CompactParams& p, int b) {
   return n;
 }
 
+// Where the moved rows of a sequence go. No cache and no list reaches 2^30 entries: a start cut to that is as far outside,
+// and its sum with a row number stays in 32 bits.
+__device__ __forceinline__ int start_of(const CompactParams& p, int b) {
+  return p.dst_start != nullptr ? min(max(__ldg(p.dst_start + b), -(1 << 30)), 1 << 30) : 0;
+}
+
 // Into another cache: every row on its own; positions past the kept rows clear
 // their weights. A warp takes 32 rows, one lane looking up each, and moves
 // them with up to eight 16-byte loads per lane in flight: the bytes bound it
@@ -247,7 +253,7 @@ __global__ void __launch_bounds__(256) compact_copy_kernel(const __grid_constant
   const int b = static_cast<int>(item / runs);
   if (b >= p.c.B) return;
   const int count = kept_count(p, b);
-  const int start = p.dst_start != nullptr ? __ldg(p.dst_start + b) : 0;
+  const int start = start_of(p, b);
   const int i = run * kCopyRows + lane;
   Place src{0, 0, false}, dst{0, 0, false};
   int from = 0;
@@ -300,7 +306,7 @@ __global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const __grid
   const int bh = blockIdx.x, b = bh / p.c.Hkv, h = bh - b * p.c.Hkv;
   const int what = blockIdx.y;  // columns of K, then of V, then the weights
   const int count = kept_count(p, b);
-  const int start = p.dst_start != nullptr ? __ldg(p.dst_start + b) : 0;
+  const int start = start_of(p, b);
   const int tid = threadIdx.x;
   if (what == cols + cols_v) {
     float* w = p.weights_out + static_cast<int64_t>(bh) * p.n_weights_out;

@@ -181,3 +181,25 @@ def test_compact_leaves_out_a_row_with_its_weight(inside, page):
     assert e.value.status == fmha.FMHA_ERR_DEVICE_INDEX
     assert torch.equal(ref.gather(ko, table, 0, room) if inside else ko[0], rows_k)
     assert torch.equal(wo, want_w)
+
+
+@pytest.mark.parametrize("start", [2 ** 31 - 1, 2 ** 31 - 3, -2 ** 31, 2 ** 30, 64])
+@pytest.mark.parametrize("inside", [True, False])
+def test_compact_to_a_start_outside_the_cache(start, inside):
+    """Sums of a start and a row number stay in range: nothing moves, no weight changes but those past a negative start."""
+    from precision_attention_fmha_b200 import fmha
+
+    k, v, n = torch.randn(1, 64, 2, 64, device=DEV).bfloat16(), torch.randn(1, 64, 2, 64, device=DEV).bfloat16(), 70
+    w = torch.rand(1, 2, n, device=DEV)
+    out = dict(k_out=torch.zeros_like(k), v_out=torch.zeros_like(v), weights_out=torch.full_like(w, 3.0))
+    to = (k, v, w) if inside else tuple(out.values())
+    before = [x.clone() for x in to]
+    if start == 64:  # past the cache, not past the weights
+        before[2][:, :, 64 + 5:] = 0
+    if start < 0 and inside:
+        before[2][:] = 0
+    fmha.cache_compact(k, v, i32([[[40, 41, 42, 50, 63]]]), i32([5]), dst_start=i32([start]), weights=w, **({} if inside else out))
+    with pytest.raises(fmha.FmhaError) as e:
+        fmha.get_device_error()
+    assert e.value.status == fmha.FMHA_ERR_DEVICE_INDEX
+    assert all(torch.equal(a, b) for a, b in zip(to, before))
