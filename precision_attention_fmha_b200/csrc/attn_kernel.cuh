@@ -1516,7 +1516,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         n = last < 0 ? 0 : min(p.n_kv_blocks, last / C::BN + 1);
       }
       if constexpr (C::RAGGED) {
-        n = min(max(__ldg(p.ctx_lens + b), 0) / C::BN, n);
+        n = min(max(__ldg(p.ctx_lens + b), 0), p.Skv) / C::BN;  // whole tiles of the context, cut to the room for it
         if (p.q_lens != nullptr && t[x].tok0 >= __ldg(p.q_lens + b)) t[x].valid = false;  // padding rows only
       }
       t[x].n_kv = t[x].valid ? n : 0;

@@ -203,3 +203,102 @@ def test_compact_to_a_start_outside_the_cache(start, inside):
         fmha.get_device_error()
     assert e.value.status == fmha.FMHA_ERR_DEVICE_INDEX
     assert all(torch.equal(a, b) for a, b in zip(to, before))
+
+
+@pytest.mark.parametrize("page", [0, 16])
+def test_packed_lengths_past_the_cache(page):
+    """Lengths outside a cache whose room is no whole number of key tiles are cut to it and reported, as with few rows."""
+    from precision_attention_fmha_b200 import fmha
+
+    B, T, Hq, Hkv, D, room = 5, 17, 16, 2, 128, 1040
+    q, k, v, _, g = make(71, B, T, Hq, Hkv, D, room, page)
+    table = None
+    if page:
+        k, v, table = to_pages(k, v, page, g)
+    given, nodes = [1500, 1040, 1030, -3, 600], [17, 17, 17, 17, 40]
+    cut, left = [1040, 1040, 1030, 0, 600], [0, 0, 10, 17, 17]
+
+    def run(ctx, nodes):
+        lse = torch.empty(B, Hq, T, device=DEV)
+        return fmha.fmha_fwd_tree(q, k, v, i32(ctx), None, i32(nodes), table, lse=lse), lse
+
+    o, lse = run(given, nodes)
+    with pytest.raises(fmha.FmhaError) as e:
+        fmha.get_device_error()
+    assert e.value.status == fmha.FMHA_ERR_DEVICE_INDEX
+    want = run(cut, left)
+    fmha.get_device_error()
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    ref.check(o, lse, ref.tree(q, k, v, cut, None, i32(left), table))
+
+
+@pytest.mark.parametrize("T", [1, 17])  # the few-row kernel alone, and with the packed one before it
+def test_bad_pages_read_zeros(T):
+    from precision_attention_fmha_b200 import fmha
+
+    B, Hq, Hkv, D, room, page = 2, 16, 2, 128, 1280, 64
+    q, k, v, _, g = make(72, B, T, Hq, Hkv, D, room, page)
+    k, v, table = to_pages(k, v, page, g)
+    k, v, zero = k.nan_to_num(0), v.nan_to_num(0), k.shape[0] - 1
+    k[-1], v[-1] = 0, 0
+    table = torch.where(table == zero, zero - 1, table).to(torch.int32)  # no sequence reads the page of zeros
+    ctx = i32([1200, 1263 - T])
+    for at, bad in ((3, 1 << 20), (18, -1), (0, k.shape[0])):
+        wrong, right = table.clone(), table.clone()
+        wrong[1, at], right[1, at] = bad, zero
+        lse, want_lse = torch.empty(B, Hq, T, device=DEV), torch.empty(B, Hq, T, device=DEV)
+        o = fmha.fmha_fwd_tree(q, k, v, ctx, page_table=wrong, lse=lse)
+        with pytest.raises(fmha.FmhaError) as e:
+            fmha.get_device_error()
+        assert e.value.status == fmha.FMHA_ERR_DEVICE_INDEX
+        want = fmha.fmha_fwd_tree(q, k, v, ctx, page_table=right, lse=want_lse)
+        fmha.get_device_error()
+        assert torch.equal(o, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("page", [0, 32])
+def test_packed_many_sequences(page):
+    """More sequences than the packed kernel orders by length; strided q, out, K and V; masks with empty rows; padding."""
+    from precision_attention_fmha_b200 import fmha
+
+    B, T, Hq, Hkv, D, room = 37, 17, 8, 1, 128, 1280
+    q, k, v, _, g = make(73, B, T + 2, Hq + 3, Hkv + 1, D, room, page)
+    q = q[:, 1:T + 1, 2:Hq + 2]
+    ctx = [(397 * b + 11 * b * b) % (room - T + 1) for b in range(B)]
+    ctx[5], ctx[6], ctx[7] = 0, 1024, room - T
+    nodes = [(T - 3 * b) % (T + 1) for b in range(B)]
+    ends = [c + n for c, n in zip(ctx, nodes)]
+    poison(k, ends), poison(v, ends)
+    table = None
+    if page:
+        k, v, table = to_pages(k, v, page, g)
+    k, v = k[:, :, 1:], v[:, :, :1]
+    for b in range(B):
+        q[b, nodes[b]:] = float("nan")
+    mask = random_tree(B, T, g)
+    wide = torch.full((B, T + 1, Hq * 2, D), 5.0, device=DEV).bfloat16()
+    lse = torch.empty(B, Hq, T, device=DEV)
+    o = fmha.fmha_fwd_tree(q, k, v, i32(ctx), mask, i32(nodes), table, out=wide[:, :T, ::2], lse=lse)
+    fmha.get_device_error()
+    ref.check(o, lse, ref.tree(q, k, v, ctx, mask, i32(nodes), table))
+    assert bool((wide[:, T:] == 5).all()) and bool((wide[:, :, 1::2] == 5).all())
+
+
+def test_packed_hidden_nodes_may_hold_anything():
+    """A drafted node that a row does not see holds NaN and infinities, behind a context on the packed tiles."""
+    from precision_attention_fmha_b200 import fmha
+
+    B, T, Hq, Hkv, D, ctx = 2, 20, 16, 2, 128, [1100, 1279]
+    q, k, v, _, g = make(74, B, T, Hq, Hkv, D, 1320)
+    mask = torch.eye(T, device=DEV, dtype=torch.uint8).expand(B, T, T).contiguous()
+    mask[:, :, 0] = 1
+    for i, n in enumerate([3, 9, 16]):
+        mask[:, :, n] = 0
+        for b in range(B):
+            k[b, ctx[b] + n] = float("nan")
+            v[b, ctx[b] + n, :, i::5] = float("nan")
+            v[b, ctx[b] + n, :, i + 1::7] = float("inf")
+    lse = torch.empty(B, Hq, T, device=DEV)
+    o = fmha.fmha_fwd_tree(q, k, v, i32(ctx), mask, lse=lse)
+    fmha.get_device_error()
+    ref.check(o, lse, ref.tree(q, k, v, ctx, mask, None, None))
