@@ -302,3 +302,48 @@ def test_packed_hidden_nodes_may_hold_anything():
     o = fmha.fmha_fwd_tree(q, k, v, i32(ctx), mask, lse=lse)
     fmha.get_device_error()
     ref.check(o, lse, ref.tree(q, k, v, ctx, mask, None, None))
+
+
+def test_many_rows_in_a_replayed_graph():
+    """One capture of a wide tree, a prompt's weights, a choice and a compaction in place; between replays the lengths, the
+    drafted nodes and the queries change. Each replay gives what the calls give, and the calls what the formulas say."""
+    from precision_attention_fmha_b200 import fmha
+
+    B, T, Hq, Hkv, D, room, page = 3, 70, 16, 2, 128, 1600, 64
+    q, k, v, _, g = make(81, B, T, Hq, Hkv, D, room, page)
+    k0, v0, table = to_pages(k, v, page, g)
+    k, v = k0.clone(), v0.clone()
+    ctx, nodes, lens = i32([10, 1400, 900]), i32([T] * B), i32([10 + T, 1400 + T, 900 + T])
+    lse = torch.empty(B, Hq, T, device=DEV)
+    weights = torch.zeros(B, Hkv, room, device=DEV)
+
+    def step():
+        o = fmha.fmha_fwd_tree(q, k, v, ctx, None, nodes, table, lse=lse)
+        fmha.key_weights(q, k, lse, weights, lens, nodes, table, accumulate=False)
+        keep, counts = fmha.evict_select(weights, lens, 200, 4, 32)
+        fmha.cache_compact(k, v, keep, counts, page_table=table, weights=weights)
+        return o, keep, counts
+
+    def fresh():
+        k.copy_(k0), v.copy_(v0), weights.fill_(9.0), lse.fill_(9.0)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for c, m in (([0, 1530, 128], [70, 70, 70]), ([1279, 1280, 1281], [64, 0, 1]), ([640, 3, 1529], [33, 70, 69])):
+        ctx.copy_(i32(c)), nodes.copy_(i32(m)), lens.copy_(i32([a + b for a, b in zip(c, m)]))
+        q.copy_(torch.randn(q.shape, generator=g, device=DEV))
+        fresh()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in (*out, lse, k, v, weights)]
+        fresh()
+        want = [*step(), lse, k, v, weights]
+        assert all(torch.equal(a.nan_to_num(7), b.nan_to_num(7)) for a, b in zip(got, want))
+        ref.check(got[0], got[3], ref.tree(q, k0, v0, c, None, i32(m), table))
+    fmha.get_device_error()
+    del graph
