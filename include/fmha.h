@@ -350,7 +350,8 @@ fmha_status fmha_quantize_nvfp4(const void* src, int64_t src_row_stride, int32_t
  *   lse (nullable): fp32 [B, Hq, T], natural-log log-sum-exp of the scaled
  *     scores; -inf for a row that sees no key, whose O row is 0.
  * What a row does not see never reaches it: keys past a sequence's end, or
- * hidden nodes of a tree, may hold infinities or NaN.
+ * hidden nodes of a tree, may hold infinities or NaN. A NaN score that it does
+ * see makes the row NaN.
  * Device errors (fmha_get_device_error): FMHA_ERR_DEVICE_INDEX for a page or
  * block index out of range (a bad page reads zeros, a bad block is left out),
  * or a length outside the cache (cut to it).                               */
@@ -482,7 +483,7 @@ fmha_status fmha_evict_select(const fmha_cache_args* args, const float* weights,
  *     weights_out past the moved ones become 0.
  * Rows that are not written to keep what they held. A position out of range,
  * or on a bad page, or (out NULL) out of order, is left out, its weight with
- * it, and reported as FMHA_ERR_DEVICE_INDEX.                                                     */
+ * it, and reported as FMHA_ERR_DEVICE_INDEX.                               */
 fmha_status fmha_cache_compact(const fmha_cache_args* args, const fmha_cache_args* out, const int32_t* keep,
                                int64_t keep_stride_b, int64_t keep_stride_h, int32_t n_keep, const int32_t* counts,
                                const int32_t* dst_start, const float* weights, int32_t n_weights, float* weights_out,
